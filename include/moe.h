@@ -88,6 +88,13 @@ typedef enum {
     MOE_OP_EXPERT_FFN_FP8 = 5
 } moe_op_t;
 
+/* Which grouped product moe_grouped_workspace_size is asked for. */
+typedef enum {
+    MOE_GROUPED_OP_MATMUL = 1,
+    MOE_GROUPED_OP_BACKWARD = 2,
+    MOE_GROUPED_OP_INT8 = 3
+} moe_grouped_op_t;
+
 /* The problem statement: T tokens, hidden size d, E experts, top-k, SwiGLU
  * width f, storage dtype (a moe_dtype_t value). */
 typedef struct {
@@ -98,6 +105,17 @@ typedef struct {
     int32_t f;
     int32_t dtype;
 } moe_problem_t;
+
+/* A matrix product grouped by expert: `rows` rows in queue order, E weight
+ * matrices [N, K], storage dtype (a moe_dtype_t value; for the 8-bit integer
+ * product the dtype of its output). */
+typedef struct {
+    int64_t rows;
+    int32_t E;
+    int32_t N;
+    int32_t K;
+    int32_t dtype;
+} moe_grouped_t;
 
 /* Optional outputs of moe_forward.  Any field may be NULL; a NULL field is
  * kept in the workspace instead.  Shapes as in moe_route / moe_dispatch. */
@@ -342,6 +360,87 @@ moe_status_t moe_quantize_weights_fp8(const moe_problem_t* p, const void* w_gate
 moe_status_t moe_expert_ffn_fp8(const moe_problem_t* p, const void* x, const int32_t* sorted_assign,
                                 const int32_t* offsets, const moe_fp8_weights_t* w, void* y_perm, void* ws,
                                 size_t ws_bytes, void* stream);
+
+/*
+ * Matrix products grouped by expert (the tall-and-skinny expert GEMMs of the
+ * Piper summary, section 1), one matrix at a time: for experts that are not
+ * a bias-free SwiGLU, and for 8-bit integer weights.
+ *
+ * The queues are those of moe_dispatch: expert e owns the rows
+ * [offsets[e], offsets[e+1]) of a matrix in queue order (x_perm); offsets
+ * [E + 1] is a device array, nondecreasing, with 0 <= offsets[0] and
+ * offsets[E] <= rows.  Queues may be empty, and a row that no queue holds
+ * is neither read nor written.  Offsets that break these rules give
+ * unspecified values in the outputs, never an access outside the arrays.
+ *
+ * Limits (MOE_ERR_UNSUPPORTED otherwise): 1 <= E <= MOE_MAX_EXPERTS;
+ * 0 <= rows <= 2^31 - 1; N and K at most MOE_GROUPED_MAX_DIM; every matrix
+ * row a whole number of 16-byte words: N and K multiples of 8 (bf16) or of 4
+ * (f32), for the 8-bit integer product K a multiple of 16 and N of 8; and a
+ * launch of fewer than 2^24 workgroups (at least rows * N and E * N * K up
+ * to 2^32 fit).  Outputs must not overlap the inputs.
+ * Workspace: moe_grouped_workspace_size of the same problem; ws may be NULL
+ * when that is 0.  No atomics: the same inputs give the same bits.
+ */
+#define MOE_GROUPED_MAX_DIM (1 << 20)
+
+/* Bytes of device workspace a grouped product `op` (a moe_grouped_op_t
+ * value) needs (0 is possible).  Host only; no HIP call. */
+moe_status_t moe_grouped_workspace_size(const moe_grouped_t* g, int32_t op, size_t* bytes);
+
+/*
+ * moe_grouped_matmul -- for every expert e and row r of its queue
+ *   c[r, n] = sum_k a[r, k] * w[e, n, k]
+ * a [rows, K], w [E, N, K], c [rows, N].  fp32 accumulation; bf16: products
+ * on bf16 MFMA, one rounding to bf16; f32: fp32 MFMA.  rows = 0 is a no-op.
+ */
+moe_status_t moe_grouped_matmul(const moe_grouped_t* g, const void* a, const void* w, const int32_t* offsets,
+                                void* c, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_grouped_matmul_backward -- the gradients of moe_grouped_matmul for the
+ * output gradient dc [rows, N]:
+ *   da[r, k] = sum_n dc[r, n] * w[e, n, k]        (rows r of expert e's queue)
+ *   dw[e, n, k] = sum over the queue's rows r of dc[r, n] * a[r, k]
+ * Either of da [rows, K] and dw [E, N, K] may be NULL (then it is not
+ * computed, and w, respectively a, may be NULL too), not both.  An empty
+ * queue gives dw[e] = 0; with rows = 0 only dw is written, and a and dc may
+ * be NULL.  Accumulation and rounding as in the forward.
+ */
+moe_status_t moe_grouped_matmul_backward(const moe_grouped_t* g, const void* a, const void* w,
+                                         const int32_t* offsets, const void* dc, void* da, void* dw, void* ws,
+                                         size_t ws_bytes, void* stream);
+
+/*
+ * moe_quantize_rows_int8 -- 8-bit integer codes of a matrix src [rows, cols]
+ * (dtype: a moe_dtype_t value), one float32 scale per row:
+ *   scales[r] = max(max_c |src[r, c]| / 127, 2^-126), 1 for an all-zero row
+ *   codes[r, c] = src[r, c] / scales[r] rounded to the nearest integer, ties
+ *     to even (both quotients rounded to float32; |code| <= 127)
+ * A row that holds a NaN or an infinity gets the scale NaN and codes 0, so
+ * that products with it are NaN.  A row is a token's activations, or an
+ * output channel's weights (w [E, N, K] is a matrix of E * N rows).  cols
+ * must be a positive multiple of 16, at most MOE_GROUPED_MAX_DIM, and rows
+ * at most 2^24 - 1 (MOE_ERR_UNSUPPORTED otherwise); src, codes and scales
+ * 16-byte aligned.  rows = 0 is a no-op.
+ */
+moe_status_t moe_quantize_rows_int8(const void* src, int64_t rows, int32_t cols, int32_t dtype, void* codes,
+                                    float* scales, void* stream);
+
+/*
+ * moe_grouped_matmul_int8 -- the product of 8-bit integer matrices with a
+ * scale for each token and each output channel: for every expert e and row r
+ * of its queue
+ *   c[r, n] = (float(sum_k a[r, k] * w[e, n, k]) * a_scales[r]) * w_scales[e, n]
+ * a [rows, K] and w [E, N, K] int8, a_scales [rows] and w_scales [E, N]
+ * float32 (moe_quantize_rows_int8 makes both), c [rows, N] of the problem's
+ * dtype.  The sum is exact (int32, so K < 131072: MOE_ERR_UNSUPPORTED
+ * otherwise) on int8 MFMA.  offsets = NULL: a dense product, every row with
+ * the one matrix w [N, K] (E must be 1).  rows = 0 is a no-op.
+ */
+moe_status_t moe_grouped_matmul_int8(const moe_grouped_t* g, const void* a, const float* a_scales, const void* w,
+                                     const float* w_scales, const int32_t* offsets, void* c, void* ws,
+                                     size_t ws_bytes, void* stream);
 
 /*
  * moe_mfma_peak -- measurement kernel, not part of the layer: `workgroups`

@@ -28,9 +28,14 @@ MOE_OP_FORWARD = 3
 MOE_OP_BACKWARD = 4
 MOE_OP_EXPERT_FFN_FP8 = 5
 
+MOE_GROUPED_OP_MATMUL = 1
+MOE_GROUPED_OP_BACKWARD = 2
+MOE_GROUPED_OP_INT8 = 3
+
 MOE_MAX_EXPERTS = 256
 MOE_MAX_TOPK = 32
 MOE_NO_ALLOC_SCRATCH_BYTES = 1 << 20
+MOE_GROUPED_MAX_DIM = 1 << 20
 
 # every function the header declares, with its ctypes signature
 _p = ctypes.c_void_p
@@ -41,6 +46,10 @@ _sz = ctypes.c_size_t
 class MoeProblem(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64), ("d", _i32), ("E", _i32), ("k", _i32), ("f", _i32),
                 ("dtype", _i32)]
+
+
+class MoeGrouped(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("E", _i32), ("N", _i32), ("K", _i32), ("dtype", _i32)]
 
 
 class MoeForwardOutputs(ctypes.Structure):
@@ -64,6 +73,7 @@ class MoeBackwardOutputs(ctypes.Structure):
 
 
 _PP = ctypes.POINTER(MoeProblem)
+_PG = ctypes.POINTER(MoeGrouped)
 
 SIGNATURES = {
     "moe_status_string": (ctypes.c_char_p, [_i32]),
@@ -84,6 +94,11 @@ SIGNATURES = {
     "moe_expert_ffn_fp8": (_i32, [_PP, _p, _p, _p, ctypes.POINTER(MoeFp8Weights), _p, _p, _sz, _p]),
     "moe_backward": (_i32, [_PP, _p, _p, _p, _p, _p, _p, ctypes.POINTER(MoeForwardState), _p,
                             ctypes.POINTER(MoeBackwardOutputs), _p, _sz, _p]),
+    "moe_grouped_workspace_size": (_i32, [_PG, _i32, ctypes.POINTER(_sz)]),
+    "moe_grouped_matmul": (_i32, [_PG, _p, _p, _p, _p, _p, _sz, _p]),
+    "moe_grouped_matmul_backward": (_i32, [_PG, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
+    "moe_quantize_rows_int8": (_i32, [_p, ctypes.c_int64, _i32, _i32, _p, _p, _p]),
+    "moe_grouped_matmul_int8": (_i32, [_PG, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
 }
 
 _lib = None

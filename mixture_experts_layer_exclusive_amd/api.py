@@ -7,6 +7,7 @@ device memory (outputs and workspace) and the stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional
 
@@ -62,6 +63,14 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(device: torch.device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _on(device: torch.device):
+    """Makes ``device`` current around a launch when it is not already (a
+    kernel starts on the current device)."""
+    if device.type != "cuda" or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
 
 
 def problem(T: int, d: int, E: int, k: int, f: int, dtype) -> L.MoeProblem:
@@ -465,6 +474,153 @@ def expert_ffn_fp8(offsets: torch.Tensor, wq: dict, k: int, x: torch.Tensor, sor
                                         _ptr(y_perm) if T else None, _ptr(ws), nbytes, _stream(dev)),
             "moe_expert_ffn_fp8")
     return y_perm
+
+
+def _grouped(op: int, rows: int, E: int, N: int, K: int, dtype, device, ws: Optional[torch.Tensor]):
+    """(problem struct, workspace, its bytes) of a grouped product."""
+    g = L.MoeGrouped(rows=rows, E=E, N=N, K=K, dtype=_DTYPES[dtype])
+    need = ctypes.c_size_t(0)
+    L.check(L.load().moe_grouped_workspace_size(ctypes.byref(g), op, ctypes.byref(need)),
+            "moe_grouped_workspace_size")
+    _expect_ws(ws, device)
+    if ws is None and need.value > 0:
+        ws = torch.empty(need.value, dtype=torch.uint8, device=device)
+    return g, ws, 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def grouped_workspace_size(op: int, rows: int, E: int, N: int, K: int, dtype) -> int:
+    """Workspace bytes of a grouped product (``op``: 1 ``grouped_matmul``, 2
+    ``grouped_matmul_backward``, 3 ``grouped_matmul_int8``, whose ``dtype``
+    is its output's)."""
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    g = L.MoeGrouped(rows=rows, E=E, N=N, K=K, dtype=_DTYPES[dtype])
+    n = ctypes.c_size_t(0)
+    L.check(L.load().moe_grouped_workspace_size(ctypes.byref(g), op, ctypes.byref(n)),
+            "moe_grouped_workspace_size")
+    return n.value
+
+
+def grouped_matmul(a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, ws: Optional[torch.Tensor] = None,
+                   c: Optional[torch.Tensor] = None):
+    """The queues' rows times their expert's matrix: c[r] = w[e] a[r] for the
+    rows r in [offsets[e], offsets[e + 1]) (``dispatch``'s offsets; a is
+    ``x_perm`` or another matrix in queue order).  a [R, K], w [E, N, K],
+    returns c [R, N].  Rows of c that no queue holds are not written."""
+    if a.dim() != 2 or w.dim() != 3:
+        raise ValueError("a must be [R, K] and w [E, N, K]")
+    R, K = a.shape
+    E, N, _ = w.shape
+    dev = a.device
+    dt = _float_dtype("a", a)
+    _expect("a", a, (R, K), dt)
+    _expect("w", w, (E, N, K), dt, dev)
+    _expect("offsets", offsets, (E + 1,), torch.int32, dev)
+    _expect("c", c, (R, N), dt, dev, required=False)
+    g, ws, nbytes = _grouped(L.MOE_GROUPED_OP_MATMUL, R, E, N, K, dt, dev, ws)
+    if c is None:
+        c = torch.empty(R, N, dtype=dt, device=dev)
+    with _on(dev):
+        L.check(L.load().moe_grouped_matmul(ctypes.byref(g), _ptr(a), _ptr(w), _ptr(offsets), _ptr(c), _ptr(ws),
+                                            nbytes, _stream(dev)), "moe_grouped_matmul")
+    return c
+
+
+def grouped_matmul_backward(a: Optional[torch.Tensor], w: Optional[torch.Tensor], offsets: torch.Tensor,
+                            dc: torch.Tensor, with_da: bool = True, with_dw: bool = True,
+                            ws: Optional[torch.Tensor] = None, out: Optional[dict] = None) -> dict:
+    """Gradients of ``grouped_matmul`` for dc [R, N]: da [R, K] (rows that no
+    queue holds are not written) and dw [E, N, K] (zero for an empty queue),
+    each None when not asked for.  Without ``with_dw`` a may be None, without
+    ``with_da`` w.  ``out`` may supply either tensor."""
+    if not (with_da or with_dw):
+        raise ValueError("with_da or with_dw is required")
+    if dc.dim() != 2 or (a is not None and a.dim() != 2) or (w is not None and w.dim() != 3):
+        raise ValueError("a must be [R, K], w [E, N, K] and dc [R, N]")
+    if (with_da and w is None) or (with_dw and a is None):
+        raise ValueError("w is required for da, and a for dw")
+    R, N = dc.shape
+    K = w.shape[2] if w is not None else a.shape[1]
+    E = w.shape[0] if w is not None else offsets.numel() - 1
+    dev = dc.device
+    dt = _float_dtype("dc", dc)
+    _expect("dc", dc, (R, N), dt)
+    _expect("a", a, (R, K), dt, dev, required=False)
+    _expect("w", w, (E, N, K), dt, dev, required=False)
+    _expect("offsets", offsets, (E + 1,), torch.int32, dev)
+    res = dict(out or {})
+    _expect("da", res.get("da"), (R, K), dt, dev, required=False)
+    _expect("dw", res.get("dw"), (E, N, K), dt, dev, required=False)
+    g, ws, nbytes = _grouped(L.MOE_GROUPED_OP_BACKWARD, R, E, N, K, dt, dev, ws)
+    if not with_da:
+        res["da"] = None
+    elif res.get("da") is None:
+        res["da"] = torch.empty(R, K, dtype=dt, device=dev)
+    if not with_dw:
+        res["dw"] = None
+    elif res.get("dw") is None:
+        res["dw"] = torch.empty(E, N, K, dtype=dt, device=dev)
+    with _on(dev):
+        L.check(L.load().moe_grouped_matmul_backward(ctypes.byref(g), _ptr(a) if R else None, _ptr(w), _ptr(offsets),
+                                                     _ptr(dc) if R else None, _ptr(res["da"]) if R else None,
+                                                     _ptr(res["dw"]), _ptr(ws), nbytes, _stream(dev)),
+                "moe_grouped_matmul_backward")
+    return res
+
+
+def quantize_rows_int8(src: torch.Tensor, codes: Optional[torch.Tensor] = None,
+                       scales: Optional[torch.Tensor] = None):
+    """8-bit integer codes (int8) and a float32 scale for each row of a bf16
+    or fp32 matrix [rows, cols]: a token's activations, or an output
+    channel's weights (``w.view(E * N, K)``)."""
+    if src.dim() != 2:
+        raise ValueError("src must be [rows, cols]")
+    rows, cols = src.shape
+    dev = src.device
+    dt = _float_dtype("src", src)
+    _expect("src", src, (rows, cols), dt)
+    _expect("codes", codes, (rows, cols), torch.int8, dev, required=False)
+    _expect("scales", scales, (rows,), torch.float32, dev, required=False)
+    if codes is None:
+        codes = torch.empty(rows, cols, dtype=torch.int8, device=dev)
+    if scales is None:
+        scales = torch.empty(rows, dtype=torch.float32, device=dev)
+    with _on(dev):
+        L.check(L.load().moe_quantize_rows_int8(_ptr(src), rows, cols, _DTYPES[dt], _ptr(codes), _ptr(scales),
+                                                _stream(dev)), "moe_quantize_rows_int8")
+    return codes, scales
+
+
+def grouped_matmul_int8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                        offsets: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
+                        ws: Optional[torch.Tensor] = None, c: Optional[torch.Tensor] = None):
+    """``grouped_matmul`` of 8-bit integer codes with a scale for each row of
+    a and each output channel of w (``quantize_rows_int8``): a int8 [R, K],
+    w int8 [E, N, K], a_scales [R], w_scales [E, N]; returns c [R, N] of
+    ``out_dtype``.  Without offsets the product is dense: w [N, K], w_scales
+    [N]."""
+    if a.dim() != 2 or w.dim() != (2 if offsets is None else 3):
+        raise ValueError("a must be [R, K] and w [E, N, K] ([N, K] without offsets)")
+    if out_dtype not in _DTYPES:
+        raise ValueError(f"out_dtype {out_dtype}, expected float32 or bfloat16")
+    R, K = a.shape
+    E = 1 if offsets is None else w.shape[0]
+    N = w.shape[-2]
+    dev = a.device
+    _expect("a", a, (R, K), torch.int8)
+    _expect("a_scales", a_scales, (R,), torch.float32, dev)
+    _expect("w", w, w.shape[:-1] + (K,), torch.int8, dev)
+    _expect("w_scales", w_scales, w.shape[:-1], torch.float32, dev)
+    _expect("offsets", offsets, (E + 1,), torch.int32, dev, required=False)
+    _expect("c", c, (R, N), out_dtype, dev, required=False)
+    g, ws, nbytes = _grouped(L.MOE_GROUPED_OP_INT8, R, E, N, K, out_dtype, dev, ws)
+    if c is None:
+        c = torch.empty(R, N, dtype=out_dtype, device=dev)
+    with _on(dev):
+        L.check(L.load().moe_grouped_matmul_int8(ctypes.byref(g), _ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales),
+                                                 _ptr(offsets), _ptr(c), _ptr(ws), nbytes, _stream(dev)),
+                "moe_grouped_matmul_int8")
+    return c
 
 
 def mfma_peak_tflops(device=None, workgroups: int = 1024, iters: int = 4000, reps: int = 3) -> float:

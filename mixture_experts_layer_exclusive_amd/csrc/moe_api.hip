@@ -162,6 +162,34 @@ size_t forward_ws(const moe_problem_t& p) {
     return b;
 }
 
+// Limits of the grouped products: rows of whole 16-byte words (int8: codes of
+// K bytes), tile rows addressed with 32-bit byte offsets, 32-bit work-item
+// counts.
+moe_status_t check_grouped(const moe_grouped_t* g, bool int8) {
+    if (g == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+    if (g->rows < 0 || g->E < 1 || g->N < 1 || g->K < 1) return MOE_ERR_INVALID_ARGUMENT;
+    if (g->dtype != MOE_DTYPE_F32 && g->dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARGUMENT;
+    if (g->E > MOE_MAX_EXPERTS || g->rows > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    if (g->N > MOE_GROUPED_MAX_DIM || g->K > MOE_GROUPED_MAX_DIM) return MOE_ERR_UNSUPPORTED;
+    if (int8) {
+        // (int32 sums of products of at most 2^14: K < 2^17)
+        if (g->K % 16 != 0 || g->N % 8 != 0 || g->K >= (1 << 17)) return MOE_ERR_UNSUPPORTED;
+    } else {
+        const int words = g->dtype == MOE_DTYPE_BF16 ? 8 : 4;
+        if (g->K % words != 0 || g->N % words != 0) return MOE_ERR_UNSUPPORTED;
+    }
+    if (grouped_grid_bound(*g) >= kMaxLaunchItems / 256) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+// The workspace of a grouped product: required only when it needs one.
+moe_status_t need_grouped_ws(const moe_grouped_t& g, int op, const void* ws, size_t ws_bytes) {
+    const size_t bytes = grouped_ws_bytes(g, op);
+    if (bytes == 0) return MOE_OK;
+    MOE_TRY(need(ws));
+    return ws_bytes < bytes ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
+}
+
 void clear_hip_error() { (void)hipGetLastError(); }
 
 // Device address of `scratch` on the device of stream s: looked up once per
@@ -584,6 +612,83 @@ moe_status_t moe_expert_ffn_fp8(const moe_problem_t* p, const void* x, const int
     MOE_LAUNCH(launch_quant_rows_fp8(x, p->T, p->d, x_q, x_exp, s));
     MOE_LAUNCH(launch_expert_ffn_fp8(*p, x_q, x_exp, sorted_assign, offsets, w->w_gate, w->w_gate_exp, w->w_up,
                                      w->w_up_exp, w->w_down, w->w_down_exp, h_q, h_sc, part, y_perm, s));
+    return MOE_OK;
+}
+
+moe_status_t moe_grouped_workspace_size(const moe_grouped_t* g, int32_t op, size_t* bytes) {
+    if (bytes == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+    if (op != MOE_GROUPED_OP_MATMUL && op != MOE_GROUPED_OP_BACKWARD && op != MOE_GROUPED_OP_INT8)
+        return MOE_ERR_INVALID_ARGUMENT;
+    MOE_TRY(check_grouped(g, op == MOE_GROUPED_OP_INT8));
+    *bytes = grouped_ws_bytes(*g, op);
+    return MOE_OK;
+}
+
+moe_status_t moe_grouped_matmul(const moe_grouped_t* g, const void* a, const void* w, const int32_t* offsets,
+                                void* c, void* ws, size_t ws_bytes, void* stream) {
+    MOE_TRY(check_grouped(g, false));
+    if (g->rows == 0) return MOE_OK;
+    MOE_TRY(need(a));
+    MOE_TRY(need(w));
+    MOE_TRY(need(offsets));
+    MOE_TRY(need(c));
+    MOE_TRY(need_grouped_ws(*g, MOE_GROUPED_OP_MATMUL, ws, ws_bytes));
+    clear_hip_error();
+    MOE_LAUNCH(launch_grouped_matmul(*g, a, w, offsets, c, ws, static_cast<hipStream_t>(stream)));
+    return MOE_OK;
+}
+
+moe_status_t moe_grouped_matmul_backward(const moe_grouped_t* g, const void* a, const void* w,
+                                         const int32_t* offsets, const void* dc, void* da, void* dw, void* ws,
+                                         size_t ws_bytes, void* stream) {
+    MOE_TRY(check_grouped(g, false));
+    if (da == nullptr && dw == nullptr && g->rows > 0) return MOE_ERR_INVALID_ARGUMENT;
+    MOE_TRY(need(offsets));
+    MOE_TRY(optional(da));
+    MOE_TRY(optional(dw));
+    if (g->rows > 0) {
+        MOE_TRY(need(dc));
+        if (da != nullptr) MOE_TRY(need(w));
+        if (dw != nullptr) MOE_TRY(need(a));
+    }
+    MOE_TRY(need_grouped_ws(*g, MOE_GROUPED_OP_BACKWARD, ws, ws_bytes));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    clear_hip_error();
+    if (da != nullptr && g->rows > 0) MOE_LAUNCH(launch_grouped_da(*g, dc, w, offsets, da, ws, s));
+    if (dw != nullptr) MOE_LAUNCH(launch_grouped_dw(*g, dc, a, offsets, dw, ws, s));
+    return MOE_OK;
+}
+
+moe_status_t moe_quantize_rows_int8(const void* src, int64_t rows, int32_t cols, int32_t dtype, void* codes,
+                                    float* scales, void* stream) {
+    if (rows < 0 || cols <= 0) return MOE_ERR_INVALID_ARGUMENT;
+    if (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARGUMENT;
+    // (one 256-lane workgroup per row at most: 32-bit work-item count)
+    if (rows > kMaxLaunchItems / 256 || cols % 16 != 0 || cols > MOE_GROUPED_MAX_DIM) return MOE_ERR_UNSUPPORTED;
+    if (rows == 0) return MOE_OK;
+    MOE_TRY(need(src));
+    MOE_TRY(need(codes));
+    MOE_TRY(need(scales));
+    clear_hip_error();
+    MOE_LAUNCH(launch_quant_rows_int8(src, rows, cols, dtype, codes, scales, static_cast<hipStream_t>(stream)));
+    return MOE_OK;
+}
+
+moe_status_t moe_grouped_matmul_int8(const moe_grouped_t* g, const void* a, const float* a_scales, const void* w,
+                                     const float* w_scales, const int32_t* offsets, void* c, void* ws,
+                                     size_t ws_bytes, void* stream) {
+    MOE_TRY(check_grouped(g, true));
+    if (offsets == nullptr && g->E != 1) return MOE_ERR_INVALID_ARGUMENT;
+    if (g->rows == 0) return MOE_OK;
+    MOE_TRY(need(a));
+    MOE_TRY(need(a_scales));
+    MOE_TRY(need(w));
+    MOE_TRY(need(w_scales));
+    MOE_TRY(optional(offsets));
+    MOE_TRY(need(c));
+    MOE_TRY(need_grouped_ws(*g, MOE_GROUPED_OP_INT8, ws, ws_bytes));
+    clear_hip_error();
+    MOE_LAUNCH(launch_grouped_int8(*g, a, a_scales, w, w_scales, offsets, c, ws, static_cast<hipStream_t>(stream)));
     return MOE_OK;
 }
 
