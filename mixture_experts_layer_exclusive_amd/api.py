@@ -7,8 +7,8 @@ device memory (outputs and workspace) and the stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -22,6 +22,9 @@ def _expect(name: str, t: Optional[torch.Tensor], shape, dtype, device=None, req
     """Checks one tensor argument against the problem before anything reaches
     the C ABI (which sees only pointers: a wrong shape or dtype there would
     make the kernels read or write out of bounds)."""
+    if (type(t) is torch.Tensor and t.shape == shape and t.dtype == dtype and
+            (device is None or t.device == device) and t.is_contiguous()):
+        return  # (the usual case, in under a microsecond)
     if t is None:
         if required:
             raise ValueError(f"{name} is required")
@@ -65,12 +68,24 @@ def _stream(device: torch.device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
-def _on(device: torch.device):
-    """Makes ``device`` current around a launch when it is not already (a
-    kernel starts on the current device)."""
-    if device.type != "cuda" or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def _launch(device: torch.device, where: str, fn, *args):
+    """Calls an entry point of the C ABI with the current stream of ``device``
+    as its last argument; ``device`` is current meanwhile (a kernel starts on
+    the current device)."""
+    if device.index == torch.cuda.current_device():
+        L.check(fn(*args, torch._C._cuda_getCurrentRawStream(device.index)), where)
+    else:
+        with torch.cuda.device(device):
+            L.check(fn(*args, torch._C._cuda_getCurrentRawStream(device.index)), where)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    """The device address of a tensor that has passed ``_expect``."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("tensors must live on the GPU")
+    return t.data_ptr()
 
 
 def problem(T: int, d: int, E: int, k: int, f: int, dtype) -> L.MoeProblem:
@@ -476,29 +491,36 @@ def expert_ffn_fp8(offsets: torch.Tensor, wq: dict, k: int, x: torch.Tensor, sor
     return y_perm
 
 
-def _grouped(op: int, rows: int, E: int, N: int, K: int, dtype, device, ws: Optional[torch.Tensor]):
-    """(problem struct, workspace, its bytes) of a grouped product."""
-    g = L.MoeGrouped(rows=rows, E=E, N=N, K=K, dtype=_DTYPES[dtype])
-    need = ctypes.c_size_t(0)
-    L.check(L.load().moe_grouped_workspace_size(ctypes.byref(g), op, ctypes.byref(need)),
-            "moe_grouped_workspace_size")
-    _expect_ws(ws, device)
-    if ws is None and need.value > 0:
-        ws = torch.empty(need.value, dtype=torch.uint8, device=device)
-    return g, ws, 0 if ws is None else ws.numel() * ws.element_size()
-
-
-def grouped_workspace_size(op: int, rows: int, E: int, N: int, K: int, dtype) -> int:
-    """Workspace bytes of a grouped product (``op``: 1 ``grouped_matmul``, 2
-    ``grouped_matmul_backward``, 3 ``grouped_matmul_int8``, whose ``dtype``
-    is its output's)."""
+@functools.lru_cache(maxsize=4096)
+def _grouped_plan(op: int, rows: int, E: int, N: int, K: int, dtype):
+    """(argument for the problem struct, workspace bytes) of a grouped
+    product: a function of the sizes alone."""
     if dtype not in _DTYPES:
         raise ValueError(f"unsupported dtype {dtype}")
     g = L.MoeGrouped(rows=rows, E=E, N=N, K=K, dtype=_DTYPES[dtype])
     n = ctypes.c_size_t(0)
     L.check(L.load().moe_grouped_workspace_size(ctypes.byref(g), op, ctypes.byref(n)),
             "moe_grouped_workspace_size")
-    return n.value
+    return ctypes.byref(g), n.value
+
+
+def grouped_workspace_size(op: int, rows: int, E: int, N: int, K: int, dtype) -> int:
+    """Workspace bytes of a grouped product (``op``: 1 ``grouped_matmul``, 2
+    ``grouped_matmul_backward``, 3 ``grouped_matmul_int8``, whose ``dtype``
+    is its output's)."""
+    return _grouped_plan(op, rows, E, N, K, dtype)[1]
+
+
+def _grouped(op: int, rows: int, E: int, N: int, K: int, dtype, device, ws: Optional[torch.Tensor]):
+    """(problem struct, workspace, its bytes) of a grouped product's call."""
+    g, need = _grouped_plan(op, rows, E, N, K, dtype)
+    if ws is None:
+        if need == 0:
+            return g, None, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        _expect_ws(ws, device)
+    return g, ws, ws.numel() * ws.element_size()
 
 
 def grouped_matmul(a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, ws: Optional[torch.Tensor] = None,
@@ -516,13 +538,13 @@ def grouped_matmul(a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, ws: 
     _expect("a", a, (R, K), dt)
     _expect("w", w, (E, N, K), dt, dev)
     _expect("offsets", offsets, (E + 1,), torch.int32, dev)
-    _expect("c", c, (R, N), dt, dev, required=False)
-    g, ws, nbytes = _grouped(L.MOE_GROUPED_OP_MATMUL, R, E, N, K, dt, dev, ws)
     if c is None:
-        c = torch.empty(R, N, dtype=dt, device=dev)
-    with _on(dev):
-        L.check(L.load().moe_grouped_matmul(ctypes.byref(g), _ptr(a), _ptr(w), _ptr(offsets), _ptr(c), _ptr(ws),
-                                            nbytes, _stream(dev)), "moe_grouped_matmul")
+        c = torch.empty((R, N), dtype=dt, device=dev)
+    else:
+        _expect("c", c, (R, N), dt, dev)
+    g, ws, nbytes = _grouped(L.MOE_GROUPED_OP_MATMUL, R, E, N, K, dt, dev, ws)
+    ptrs = (_addr(a), _addr(w), _addr(offsets), _addr(c), _addr(ws))
+    _launch(dev, "moe_grouped_matmul", L.load().moe_grouped_matmul, g, *ptrs, nbytes)
     return c
 
 
@@ -555,16 +577,14 @@ def grouped_matmul_backward(a: Optional[torch.Tensor], w: Optional[torch.Tensor]
     if not with_da:
         res["da"] = None
     elif res.get("da") is None:
-        res["da"] = torch.empty(R, K, dtype=dt, device=dev)
+        res["da"] = torch.empty((R, K), dtype=dt, device=dev)
     if not with_dw:
         res["dw"] = None
     elif res.get("dw") is None:
-        res["dw"] = torch.empty(E, N, K, dtype=dt, device=dev)
-    with _on(dev):
-        L.check(L.load().moe_grouped_matmul_backward(ctypes.byref(g), _ptr(a) if R else None, _ptr(w), _ptr(offsets),
-                                                     _ptr(dc) if R else None, _ptr(res["da"]) if R else None,
-                                                     _ptr(res["dw"]), _ptr(ws), nbytes, _stream(dev)),
-                "moe_grouped_matmul_backward")
+        res["dw"] = torch.empty((E, N, K), dtype=dt, device=dev)
+    # (an empty tensor has no address)
+    ptrs = (_addr(a), _addr(w), _addr(offsets), _addr(dc), _addr(res["da"]), _addr(res["dw"]), _addr(ws))
+    _launch(dev, "moe_grouped_matmul_backward", L.load().moe_grouped_matmul_backward, g, *ptrs, nbytes)
     return res
 
 
@@ -579,15 +599,16 @@ def quantize_rows_int8(src: torch.Tensor, codes: Optional[torch.Tensor] = None,
     dev = src.device
     dt = _float_dtype("src", src)
     _expect("src", src, (rows, cols), dt)
-    _expect("codes", codes, (rows, cols), torch.int8, dev, required=False)
-    _expect("scales", scales, (rows,), torch.float32, dev, required=False)
     if codes is None:
-        codes = torch.empty(rows, cols, dtype=torch.int8, device=dev)
+        codes = torch.empty((rows, cols), dtype=torch.int8, device=dev)
+    else:
+        _expect("codes", codes, (rows, cols), torch.int8, dev)
     if scales is None:
-        scales = torch.empty(rows, dtype=torch.float32, device=dev)
-    with _on(dev):
-        L.check(L.load().moe_quantize_rows_int8(_ptr(src), rows, cols, _DTYPES[dt], _ptr(codes), _ptr(scales),
-                                                _stream(dev)), "moe_quantize_rows_int8")
+        scales = torch.empty((rows,), dtype=torch.float32, device=dev)
+    else:
+        _expect("scales", scales, (rows,), torch.float32, dev)
+    ptrs = (_addr(src), rows, cols, _DTYPES[dt], _addr(codes), _addr(scales))
+    _launch(dev, "moe_quantize_rows_int8", L.load().moe_quantize_rows_int8, *ptrs)
     return codes, scales
 
 
@@ -612,14 +633,13 @@ def grouped_matmul_int8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor
     _expect("w", w, w.shape[:-1] + (K,), torch.int8, dev)
     _expect("w_scales", w_scales, w.shape[:-1], torch.float32, dev)
     _expect("offsets", offsets, (E + 1,), torch.int32, dev, required=False)
-    _expect("c", c, (R, N), out_dtype, dev, required=False)
-    g, ws, nbytes = _grouped(L.MOE_GROUPED_OP_INT8, R, E, N, K, out_dtype, dev, ws)
     if c is None:
-        c = torch.empty(R, N, dtype=out_dtype, device=dev)
-    with _on(dev):
-        L.check(L.load().moe_grouped_matmul_int8(ctypes.byref(g), _ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales),
-                                                 _ptr(offsets), _ptr(c), _ptr(ws), nbytes, _stream(dev)),
-                "moe_grouped_matmul_int8")
+        c = torch.empty((R, N), dtype=out_dtype, device=dev)
+    else:
+        _expect("c", c, (R, N), out_dtype, dev)
+    g, ws, nbytes = _grouped(L.MOE_GROUPED_OP_INT8, R, E, N, K, out_dtype, dev, ws)
+    ptrs = (_addr(a), _addr(a_scales), _addr(w), _addr(w_scales), _addr(offsets), _addr(c), _addr(ws))
+    _launch(dev, "moe_grouped_matmul_int8", L.load().moe_grouped_matmul_int8, g, *ptrs, nbytes)
     return c
 
 

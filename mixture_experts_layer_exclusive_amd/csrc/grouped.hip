@@ -11,180 +11,14 @@
 // W in kNN, both operands in kTN).  One pipeline serves all of them; only how
 // a slice is laid out in LDS and read into fragments differs.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
-#include "device_util.h"
-#include "lds_dma.h"
-#include "moe_internal.h"
+#include "grouped_common.h"
 
 namespace moe {
 
 namespace {
-
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
-typedef float f32x16_t __attribute__((ext_vector_type(16)));
-typedef int i32x4_t __attribute__((ext_vector_type(4)));
-typedef int i32x16_t __attribute__((ext_vector_type(16)));
-
-constexpr int kNT = 0, kNN = 1, kTN = 2;
-constexpr int kBf16 = 0, kF32 = 1, kI8 = 2;
-constexpr int kXcds = 8;
-constexpr int kGroupM = 8;  // row tiles per group of the tile order
-
-// ---- queues and the tile order ---------------------------------------------
-
-// The queues in LDS: clamped to the matrix, so that no offsets, whatever they
-// hold, lead outside it (0 <= lo <= hi <= rows), and the prefix sums of their
-// row tiles.
-struct Queues {
-    int prefix[MOE_MAX_EXPERTS + 1];
-    int lo[MOE_MAX_EXPERTS];
-    int hi[MOE_MAX_EXPERTS];
-};
-
-// Filled by the first wave (lane l: experts 4l .. 4l + 3, all loads together),
-// then a barrier.  offsets = NULL: one queue of all rows.
-__device__ __forceinline__ void build_queues(const int32_t* __restrict__ offsets, int E, int rows, int bm, Queues& q) {
-    if (threadIdx.x < 64) {
-        const int lane = threadIdx.x;
-        int o[5];
-        if (offsets != nullptr) {
-#pragma unroll
-            for (int i = 0; i < 5; ++i) o[i] = offsets[min(lane * 4 + i, E)];
-        } else {
-#pragma unroll
-            for (int i = 0; i < 5; ++i) o[i] = lane * 4 + i == 0 ? 0 : rows;
-        }
-        int lo[4], hi[4], c[4], local = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            lo[i] = min(max(o[i], 0), rows);
-            hi[i] = max(min(o[i + 1], rows), lo[i]);
-            c[i] = lane * 4 + i < E ? (hi[i] - lo[i] + bm - 1) / bm : 0;
-            local += c[i];
-        }
-        int incl = local;
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-            const int v = __shfl_up(incl, off, 64);
-            if (lane >= off) incl += v;
-        }
-        int run = incl - local;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = lane * 4 + i;
-            if (e < E) {
-                q.prefix[e] = run;
-                q.lo[e] = lo[i];
-                q.hi[e] = hi[i];
-            }
-            run += c[i];
-        }
-        if (lane == 63) q.prefix[E] = incl;
-    }
-    __syncthreads();
-}
-
-// An output tile: rows [m0, m1) and columns from p0, of expert e, summed over
-// q0 .. q1 (kTN: queue rows; otherwise 0 .. the reduction length).
-struct Tile {
-    int e, m0, m1, p0, q0, q1;
-};
-
-// kNT, kNN: workgroups are dealt to the 8 XCDs round-robin; the id is remapped
-// so that each XCD walks one contiguous range of the tile order, which groups
-// kGroupM row tiles per column tile: the tiles running on one XCD at a time
-// share operand rows in its L2.
-__device__ __forceinline__ bool find_row_tile(const Queues& q, int E, int bm, int bn, int P, Tile& t) {
-    const int ptiles = (P + bn - 1) / bn;
-    const int total_m = q.prefix[E];
-    // (the launch holds total_m * ptiles below 2^24 workgroups for every
-    // offsets that keeps the rules; others may ask for more, and then only
-    // the tiles of this grid are computed)
-    const int64_t total = static_cast<int64_t>(total_m) * ptiles;
-    const int64_t per_xcd = (total + kXcds - 1) / kXcds;
-    const int64_t place = blockIdx.x / kXcds;
-    const int64_t pid64 = (blockIdx.x % kXcds) * per_xcd + place;
-    if (place >= per_xcd || pid64 >= total || pid64 > 0x7fffffff) return false;
-    const int pid = static_cast<int>(pid64);
-    const int group = pid / (kGroupM * ptiles);
-    const int first = group * kGroupM;
-    const int gsz = min(kGroupM, total_m - first);
-    const int local = pid - group * kGroupM * ptiles;
-    const int mt = first + local % gsz;
-    int lo = 0, hi = E;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (q.prefix[mid] <= mt) lo = mid; else hi = mid;
-    }
-    t.e = lo;
-    t.m0 = q.lo[lo] + (mt - q.prefix[lo]) * bm;
-    t.m1 = min(t.m0 + bm, q.hi[lo]);
-    t.p0 = (local / gsz) * bn;
-    // (always so unless broken offsets overflowed the prefix sums)
-    return t.m0 >= q.lo[lo] && t.m0 < t.m1;
-}
-
-// ---- global -> LDS -----------------------------------------------------------
-
-// A buffer descriptor over the 2^31 bytes from base: a lane whose offset is
-// 2^31 or more is out of range, reads nothing and puts zeros into LDS.  That
-// is how rows past a queue, columns past a matrix and the end of the reduction
-// become zeros in both operands (a zero in one alone would not do: zero times
-// the infinity or NaN of whatever lies there is NaN).
-constexpr uint32_t kOutOfRange = 0x80000000u;
-constexpr uint32_t kRsrcWord3 = 0x00020000u;  // raw buffer, 32-bit data format
-
-// 16 bytes per lane from base + voff into LDS at lds_base + 16 * lane.  Inline
-// assembly so that the compiler does not take every later LDS read for
-// dependent on it; ordered by wait_vmcnt and the workgroup barrier.  The
-// descriptor comes from scalar instructions, and s_nop covers the wait state
-// between a scalar write of M0 and its use.
-__device__ __forceinline__ void lds_dma16_b(uint64_t base, uint32_t voff, uint32_t lds_base) {
-    i32x4_t rsrc;
-    rsrc[0] = static_cast<int>(static_cast<uint32_t>(base));
-    rsrc[1] = static_cast<int>(static_cast<uint32_t>(base >> 32) & 0xffffu);
-    rsrc[2] = static_cast<int>(kOutOfRange);
-    rsrc[3] = static_cast<int>(kRsrcWord3);
-    asm volatile(
-        "s_nop 0\n\t"
-        "buffer_load_dwordx4 %0, %1, 0 offen lds"
-        :
-        : "v"(voff), "s"(rsrc), "{m0}"(lds_base)
-        : "memory");
-}
-
-__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
-    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
-    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
-    return (static_cast<uint64_t>(hi) << 32) | lo;
-}
-
-// LDS slot of 16-byte chunk c of row r in a row-major slice (128-byte rows):
-// c ^ row_swizzle(r), which spreads a fragment read's 32 rows over the banks.
-__device__ __forceinline__ int row_swizzle(int r) { return (r >> 1) & 7; }
-
-// The same in a column-major bf16 slice of CH chunks per row: the transposing
-// reads of one instruction touch 4 neighbouring rows; flipping chunk bits 2-3
-// by r & 3 puts them on different banks.
-template <int CH>
-__device__ __forceinline__ int col_swizzle(int r) {
-    return ((r & 3) << 2) & (CH - 1);
-}
-
-__device__ __forceinline__ f32x16_t zero16(f32x16_t) {
-    f32x16_t v;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.f;
-    return v;
-}
-__device__ __forceinline__ i32x16_t zero16(i32x16_t) {
-    i32x16_t v;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0;
-    return v;
-}
 
 // ---- the tile kernel ------------------------------------------------------------
 //
@@ -193,415 +27,834 @@ __device__ __forceinline__ i32x16_t zero16(i32x16_t) {
 // two LDS stages.  The MFMA takes Y's fragment first and X's second, so a lane
 // holds one output row (lane & 31) and runs of 4 consecutive columns.
 //
+// A workgroup walks tiles `place`, `place` + gridDim / 8, ... of its XCD, and
+// the slices of all its tiles are one stream: while a tile's last slices are
+// multiplied and its outputs stored, the first slices of the next are landing.
+//
 // Each slice has 4 steps of 32 bytes of q (16 bytes per half wave).  Step 0
-// multiplies fragments read during the slice before, while the fragments of
-// steps 1-3 are read; then the stage is free, and the loads of the
-// next-but-one slice go out spread over steps 1-3 (an LDS-bound load holds up
-// the MFMAs behind it, so a burst of them stalls); before step 3 the next
-// slice has landed, and step 3 reads its first fragments.
-template <int TY, int MODE, int MB, int NB, typename O>
+// multiplies fragments read during the slice before; the fragments of steps 1
+// and 2 are read during step 0, those of step 3 early in step 1 (all of them
+// in step 0 would take longer than its MFMAs: 24 KB per wave at 128 bytes a
+// clock).  Then the stage is free, and the loads of the next-but-one slice go
+// out spread over the other MFMAs (an LDS-bound load holds up the MFMAs
+// behind it, so a burst of them stalls).  Before step 3 the next slice has
+// landed, and step 3 reads its first fragments.
+template <int TY, int MODE, int MB, int NB, int NS, typename O>
 __global__ __launch_bounds__(256, (MB * NB > 4 ? 1 : 2)) void grouped_tile_kernel(
     const void* __restrict__ Xp, const void* __restrict__ Yp, const int32_t* __restrict__ offsets, int E, int rows,
-    int N, int K, O* __restrict__ C, const float* __restrict__ sx, const float* __restrict__ sy) {
-    constexpr int EB = TY == kBf16 ? 2 : (TY == kF32 ? 4 : 1);
+    int N, int K, O* __restrict__ C, const float* __restrict__ sx, const float* __restrict__ sy, int parts) {
     constexpr bool XC = MODE == kTN;             // X column-major
     constexpr bool YC = MODE != kNT;             // Y column-major
     static_assert(TY != kI8 || MODE == kNT, "int8: forward only");
     constexpr int TM = 64 * MB, TN = 64 * NB;    // output tile
+    using XS = Slice<TY, XC, TM>;
+    using YS = Slice<TY, YC, TN>;
+    constexpr int EB = XS::EB;
     constexpr int QS = 128 / EB;                 // q per slice
-    constexpr int XL = TM / 32, YL = TN / 32;    // loads per wave and slice (1 KB each)
+    constexpr int XL = XS::LOADS / 4, YL = YS::LOADS / 4;  // loads per wave and slice
     constexpr int NL = XL + YL;
     constexpr int X_BYTES = TM * 128;
     constexpr int STAGE = (TM + TN) * 128;
-    constexpr int XCH = TM * EB / 16, YCH = TN * EB / 16;  // chunks per column-major row
     constexpr int NM = MB * NB;
     constexpr int NR = MB + NB;
-    using Acc = std::conditional_t<TY == kI8, i32x16_t, f32x16_t>;
-    __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
-    static_assert(sizeof(Queues) <= 2 * STAGE, "the queues' table lives in the stages until the first load");
-    Queues& queues = *reinterpret_cast<Queues*>(smem);
-
-    Tile t;
-    t.q0 = 0;
-    t.q1 = MODE == kNT ? K : N;
-    build_queues(offsets, E, rows, TM, queues);
-    if constexpr (MODE == kTN) {
-        const int mt = (N + TM - 1) / TM, pt = (K + TN - 1) / TN;
-        const int per_e = mt * pt;
-        t.e = blockIdx.x / per_e;
-        const int l = blockIdx.x % per_e;
-        t.m0 = (l % mt) * TM;
-        t.m1 = min(t.m0 + TM, N);
-        t.p0 = (l / mt) * TN;
-        t.q0 = queues.lo[t.e];
-        t.q1 = queues.hi[t.e];
-    } else {
-        if (!find_row_tile(queues, E, TM, TN, MODE == kNT ? N : K, t)) return;
-    }
-    const int e = __builtin_amdgcn_readfirstlane(t.e);
-    const int m0 = __builtin_amdgcn_readfirstlane(t.m0), m1 = __builtin_amdgcn_readfirstlane(t.m1);
-    const int p0 = __builtin_amdgcn_readfirstlane(t.p0);
-    const int q0 = __builtin_amdgcn_readfirstlane(t.q0), q1 = __builtin_amdgcn_readfirstlane(t.q1);
-    __syncthreads();  // every lookup is done before the loads overwrite the table
+    constexpr bool BF_OUT = sizeof(O) == 2;
+    constexpr int NP = BF_OUT && NB >= 2 ? 2 : 1;  // column blocks the epilogue stages at a time
+    constexpr int EROW = NP * 32 * sizeof(O);    // bytes of a staged row: a 128-byte line (bf16, NB = 1: 64)
+    constexpr int CPR = EROW / 16;               // 16-byte chunks per staged row
+    constexpr int RPS = 64 / CPR;                // rows per store
+    constexpr int EPI = 32 * EROW;               // staged bytes per wave
+    // the largest tiles walk the tile order as one stream and stage their
+    // outputs beside the stages; the others take one tile and stage over them
+    constexpr bool STREAM = NM > 4;
+    constexpr int EPI_AT = STREAM ? NS * STAGE : 0;
+    constexpr int Q_AT = NS * STAGE + (STREAM ? 4 * EPI : 0);
+    static_assert(4 * EPI <= NS * STAGE, "the staged outputs must fit the stages");
+    __shared__ __attribute__((aligned(1024))) char smem[Q_AT + sizeof(Queues) + 512];
+    static_assert(sizeof(smem) <= 160 * 1024, "LDS");
+    Queues& queues = *reinterpret_cast<Queues*>(smem + Q_AT);
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 1, wn = wave & 1;
-    const int half = lane >> 5, l32 = lane & 31;
     const int P = MODE == kNT ? N : K;           // output columns
     const int64_t xrow = static_cast<int64_t>(MODE == kNT ? K : N) * EB;  // bytes of an operand's memory row
     const int64_t yrow = static_cast<int64_t>(K) * EB;
 
-    // ---- loads: load j of this wave fills 1 KB at (wave * L + j) * 1024 of the
-    // operand's part of the stage
-    const int nk = (q1 - q0 + QS - 1) / QS;
-    const int qtail = q1 - q0 - (nk - 1) * QS;   // q in the last slice
-    uint32_t xoff[XL], yoff[YL];
-    uint32_t xtail = 0, ytail = 0;               // bit j: out of range in the last slice
-    uint64_t xbase, ybase;
-    int64_t xstep = 128, ystep = 128;
-    if constexpr (XC) {
-        xstep = QS * xrow;
-        xbase = reinterpret_cast<uint64_t>(Xp) + static_cast<uint64_t>(q0 * xrow + static_cast<int64_t>(m0) * EB);
-#pragma unroll
-        for (int j = 0; j < XL; ++j) {
-            const int r = (wave * XL + j) * (64 / XCH) + lane / XCH;
-            const int c = (lane % XCH) ^ (TY == kBf16 ? col_swizzle<XCH>(r) : 0);
-            xoff[j] = static_cast<uint32_t>(r) * static_cast<uint32_t>(xrow) + c * 16;
-            if (m0 + c * (16 / EB) >= N) xoff[j] = kOutOfRange;
-            xtail |= (r >= qtail ? 1u : 0u) << j;
+    load_queues<MODE == kTN>(offsets, E, rows, TM, queues);
+    const int xcd = blockIdx.x % kXcds;
+    const int stride = gridDim.x / kXcds;
+    auto tile_at = [&](int place, Tile& t) -> Found {
+        if constexpr (MODE == kTN) {
+            return weight_tile(queues, E, N, K, TM, TN, QS, parts, xcd, place, t);
+        } else {
+            t.q0 = 0;
+            t.q1 = MODE == kNT ? K : N;
+            return row_tile(queues, E, TM, TN, P, xcd, place, t);
         }
-    } else {
-        xbase = reinterpret_cast<uint64_t>(Xp) + static_cast<uint64_t>(m0 * xrow);
-#pragma unroll
-        for (int j = 0; j < XL; ++j) {
-            const int r = (wave * XL + j) * 8 + (lane >> 3);
-            const int c = (lane & 7) ^ row_swizzle(r);
-            xoff[j] = static_cast<uint32_t>(r) * static_cast<uint32_t>(xrow) + c * 16;
-            if (m0 + r >= m1) xoff[j] = kOutOfRange;
-            xtail |= (c * (16 / EB) >= qtail ? 1u : 0u) << j;
-        }
-    }
-    if constexpr (YC) {
-        ystep = QS * yrow;
-        ybase = reinterpret_cast<uint64_t>(Yp) +
-                static_cast<uint64_t>((MODE == kTN ? q0 : static_cast<int64_t>(e) * N) * yrow + static_cast<int64_t>(p0) * EB);
-#pragma unroll
-        for (int j = 0; j < YL; ++j) {
-            const int r = (wave * YL + j) * (64 / YCH) + lane / YCH;
-            const int c = (lane % YCH) ^ (TY == kBf16 ? col_swizzle<YCH>(r) : 0);
-            yoff[j] = static_cast<uint32_t>(r) * static_cast<uint32_t>(yrow) + c * 16;
-            if (p0 + c * (16 / EB) >= P) yoff[j] = kOutOfRange;
-            ytail |= (r >= qtail ? 1u : 0u) << j;
-        }
-    } else {
-        ybase = reinterpret_cast<uint64_t>(Yp) + static_cast<uint64_t>((static_cast<int64_t>(e) * N + p0) * yrow);
-#pragma unroll
-        for (int j = 0; j < YL; ++j) {
-            const int r = (wave * YL + j) * 8 + (lane >> 3);
-            const int c = (lane & 7) ^ row_swizzle(r);
-            yoff[j] = static_cast<uint32_t>(r) * static_cast<uint32_t>(yrow) + c * 16;
-            if (p0 + r >= P) yoff[j] = kOutOfRange;
-            ytail |= (c * (16 / EB) >= qtail ? 1u : 0u) << j;
-        }
-    }
-    xbase = uniform64(xbase);
-    ybase = uniform64(ybase);
-    // (a scalar register that a vector instruction has written, as
-    // readfirstlane does, may be read by a load 5 wait states later)
-    asm volatile("s_nop 4" : "+s"(xbase), "+s"(ybase));
+    };
+
+    // (an empty queue's weight gradient is one slice that is out of range
+    // altogether: zeros)
+    auto slices_of = [&](const Tile& t) { return max((t.q1 - t.q0 + QS - 1) / QS, 1); };
+
+    // ---- the load side: the tile being loaded, and how much of it is left
+    constexpr int64_t kLineStep = 128;
+    const int64_t xstep = XC ? QS * xrow : kLineStep, ystep = YC ? QS * yrow : kLineStep;
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
     const uint32_t lds_x = lds0 + wave * (XL * 1024);
     const uint32_t lds_y = lds0 + X_BYTES + wave * (YL * 1024);
-    // load l (< NL) of slice kt
-    auto dma = [&](int l, int kt) {
-        const uint32_t so = (kt & 1) * STAGE;
-        const bool last = kt == nk - 1;
-        if (l < YL) {
-            const uint32_t tm = last ? ytail : 0u;
-            lds_dma16_b(ybase + kt * ystep, yoff[l < YL ? l : 0] | ((tm << (31 - l)) & kOutOfRange), lds_y + so + l * 1024);
-        } else {
-            const int j = l - YL;
-            const uint32_t tm = last ? xtail : 0u;
-            lds_dma16_b(xbase + kt * xstep, xoff[j < XL && j >= 0 ? j : 0] | ((tm << (31 - j)) & kOutOfRange),
-                        lds_x + so + j * 1024);
+    int lplace = blockIdx.x / kXcds;
+    int left = 0;                                // slices still to load
+    uint64_t xbase = 0, ybase = 0;
+    // This wave's loads j fill the KB at (wave * L + j) * 1024 of the operand's
+    // part of the stage.  Bit j of the tail masks: the lane's part of load j is
+    // out of range in the tile's last slice.
+    uint32_t xoff[XL], yoff[YL], xtail = 0, ytail = 0;
+    bool tailed = false;                         // the last slice is not a whole one
+    auto aim = [&](const Tile& t) {
+        left = slices_of(t);
+        const int qtail = t.q1 - t.q0 - (left - 1) * QS;  // q in the last slice
+        int ln = lane;
+        asm volatile("" : "+v"(ln));  // (keeps the lane's part from being computed ahead and held in registers)
+        xtail = ytail = 0;
+        tailed = qtail < QS;
+        xbase = reinterpret_cast<uint64_t>(Xp) +
+                static_cast<uint64_t>(XC ? t.q0 * xrow + static_cast<int64_t>(t.m0) * EB : t.m0 * xrow);
+        ybase = reinterpret_cast<uint64_t>(Yp) +
+                static_cast<uint64_t>(MODE == kTN   ? t.q0 * yrow + static_cast<int64_t>(t.p0) * EB
+                                      : MODE == kNN ? static_cast<int64_t>(t.e) * N * yrow + static_cast<int64_t>(t.p0) * EB
+                                                    : (static_cast<int64_t>(t.e) * N + t.p0) * yrow);
+#pragma unroll
+        for (int j = 0; j < XL; ++j) {
+            xoff[j] = XS::offset(wave * XL + j, ln, static_cast<uint32_t>(xrow), t.m1 - t.m0);
+            xtail |= (XS::beyond(wave * XL + j, ln, qtail) ? 1u : 0u) << j;
         }
+#pragma unroll
+        for (int j = 0; j < YL; ++j) {
+            yoff[j] = YS::offset(wave * YL + j, ln, static_cast<uint32_t>(yrow), P - t.p0);
+            ytail |= (YS::beyond(wave * YL + j, ln, qtail) ? 1u : 0u) << j;
+        }
+        xbase = uniform64(xbase);
+        ybase = uniform64(ybase);
     };
-
-    // ---- fragment reads
-    uint32_t foff[4];                            // row-major: per step
+    auto nothing = [&]() {
+        left = 0x7fffffff;
+        tailed = false;
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) foff[kk] = l32 * 128 + (((2 * kk + half) ^ row_swizzle(l32)) * 16);
-    // column-major bf16: a fragment (32 columns x 16 q) is two transposing
-    // reads: in each 16-lane group g (lanes 16 g + i), lane i addresses q row
-    // (g >> 1) * 8 + (i >> 2) (+ 4 in the second read) and columns (g & 1) * 16
-    // + 4 (i & 3) .. + 4, and receives column (g & 1) * 16 + i at 4 rows.
-    uint32_t xcof[XC && TY == kBf16 ? MB : 1], ycof[YC && TY == kBf16 ? NB : 1];
-    {
-        const int g = lane >> 4, i = lane & 15;
-        const int r = (g >> 1) * 8 + (i >> 2);
-        const int low = (g & 1) * 2 + ((i & 3) >> 1);
-        if constexpr (XC && TY == kBf16) {
+        for (int j = 0; j < XL; ++j) xoff[j] = kOutOfRange;
 #pragma unroll
-            for (int b = 0; b < MB; ++b)
-                xcof[b] = r * (TM * EB) + ((((wm * MB + b) * 4 + low) ^ col_swizzle<XCH>(r)) << 4) + 8 * (i & 1);
-        }
-        if constexpr (YC && TY == kBf16) {
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-                ycof[b] = X_BYTES + r * (TN * EB) + ((((wn * NB + b) * 4 + low) ^ col_swizzle<YCH>(r)) << 4) + 8 * (i & 1);
-        }
-    }
-    i32x4_t f[4][NR];  // f[step][X blocks, then Y blocks]
-    auto read_frag = [&](int kk, int i, uint32_t so) {
-        const bool is_x = i < MB;
-        const int b = is_x ? i : i - MB;
-        if ((is_x && !XC) || (!is_x && !YC)) {
-            const char* base = smem + so + (is_x ? (wm * MB + b) * 32 * 128 : X_BYTES + (wn * NB + b) * 32 * 128);
-            f[kk][i] = *reinterpret_cast<const i32x4_t*>(base + foff[kk]);
-        } else if constexpr (TY == kBf16) {
-            typedef short s4_t __attribute__((ext_vector_type(4)));
-            typedef __attribute__((address_space(3))) s4_t* lds_s4_t;
-            constexpr int XB = TM * EB, YB = TN * EB;
-            const int rb = is_x ? XB : YB;
-            const uint32_t a = lds_addr(smem) + so + (is_x ? xcof[is_x && XC ? b : 0] : ycof[!is_x && YC ? b : 0]) + kk * 16 * rb;
-            const s4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s4_t>(a));
-            const s4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s4_t>(a + 4 * rb));
-            f[kk][i] = __builtin_bit_cast(i32x4_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-        } else {
-            const int rb = (is_x ? TM : TN) * EB;
-            const char* base = smem + so + (is_x ? (wm * MB + b) * 128 : X_BYTES + (wn * NB + b) * 128) + l32 * 4;
-#pragma unroll
-            for (int i4 = 0; i4 < 4; ++i4)
-                f[kk][i][i4] = *reinterpret_cast<const int*>(base + (8 * kk + 4 * half + i4) * rb);
-        }
+        for (int j = 0; j < YL; ++j) yoff[j] = kOutOfRange;
     };
-
-    Acc acc[NB][MB];
-#pragma unroll
-    for (int a = 0; a < NB; ++a)
-#pragma unroll
-        for (int b = 0; b < MB; ++b) acc[a][b] = zero16(Acc{});
-    auto mul = [&](int kk, int q) {
-        const int nb = q / MB, mb = q % MB;
-        if constexpr (TY == kBf16) {
-            acc[nb][mb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, f[kk][MB + nb]),
-                                                                  __builtin_bit_cast(bf16x8_t, f[kk][mb]), acc[nb][mb], 0, 0, 0);
-        } else if constexpr (TY == kI8) {
-            acc[nb][mb] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f[kk][MB + nb], f[kk][mb], acc[nb][mb], 0, 0, 0);
-        } else {
-            const f32x4_t y = __builtin_bit_cast(f32x4_t, f[kk][MB + nb]), x = __builtin_bit_cast(f32x4_t, f[kk][mb]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                acc[nb][mb] = __builtin_amdgcn_mfma_f32_32x32x2f32(y[i], x[i], acc[nb][mb], 0, 0, 0);
-        }
-    };
-
-    // loads issued by the end of slot p of the 3 NM slots of steps 1..3
-    auto refill = [&](int p, int kt) {
-#pragma unroll
-        for (int l = p * NL / (3 * NM); l < (p + 1) * NL / (3 * NM); ++l) dma(l, kt + 2);
-    };
-    constexpr int BEFORE3 = 2 * NM * NL / (3 * NM);
-
-    if (nk > 0) {
-#pragma unroll
-        for (int l = 0; l < NL; ++l) dma(l, 0);
-        if (nk > 1) {
-#pragma unroll
-            for (int l = 0; l < NL; ++l) dma(l, 1);
-            wait_vmcnt<NL>();
-        } else {
-            wait_vmcnt<0>();
-        }
-        barrier_lds();
-#pragma unroll
-        for (int i = 0; i < NR; ++i) read_frag(0, i, 0);
-        __builtin_amdgcn_sched_barrier(0);
-    }
-    auto slice = [&](int kt, auto more_c) {
-        constexpr bool MORE = decltype(more_c)::value;
-        const uint32_t so = (kt & 1) * STAGE, nso = ((kt + 1) & 1) * STAGE;
-#pragma unroll
-        for (int kk = 1; kk < 4; ++kk)
-#pragma unroll
-            for (int i = 0; i < NR; ++i) read_frag(kk, i, so);
-#pragma unroll
-        for (int q = 0; q < NM; ++q) mul(0, q);
-        __builtin_amdgcn_sched_barrier(0);
-        wait_vmcnt_lgkm0<63>();
-        barrier_lds();
-#pragma unroll
-        for (int step = 1; step <= 2; ++step) {
-#pragma unroll
-            for (int q = 0; q < NM; ++q) {
-                mul(step, q);
-                if (MORE) {
-                    refill((step - 1) * NM + q, kt);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
+    // the tiles between the load side and the multiplying side (at most two, of
+    // one slice each, and the one being multiplied), kept by each wave for itself
+    int* const ring = reinterpret_cast<int*>(smem + Q_AT + sizeof(Queues)) + wave * 32;
+    int loading = 0;                             // tiles the load side has begun
+    // the next tile; after the last, every load is out of range
+    auto next_load = [&]() {
+        for (;;) {
+            Tile t;
+            const Found f = tile_at(lplace, t);
+            lplace += stride;
+            if (f == kTile) {
+                aim(t);
+                int* const r = ring + (loading & 3) * 8;
+                *reinterpret_cast<i32x4_t*>(r) = i32x4_t{t.e, t.m0, t.m1, t.p0};
+                r[4] = left;
+                ++loading;
+                return;
             }
+            if (f == kEnd) {
+                nothing();
+                return;
+            }
+        }
+    };
+    // load l (< NL) of the next slice to load, into stage `so`
+    auto dma = [&](int l, uint32_t so) {
+        const bool y = l < YL;
+        const int j = y ? l : l - YL;
+        lds_dma16_b(y ? ybase : xbase, y ? yoff[j < YL ? j : 0] : xoff[j < XL ? j : 0],
+                    (y ? lds_y : lds_x) + so + j * 1024);
+    };
+    // before a tile's last slice is loaded (its offsets are not needed again)
+    auto cut_tail = [&]() {
+        if (left == 1 && tailed) {
+#pragma unroll
+            for (int j = 0; j < XL; ++j) xoff[j] |= (xtail << (31 - j)) & kOutOfRange;
+#pragma unroll
+            for (int j = 0; j < YL; ++j) yoff[j] |= (ytail << (31 - j)) & kOutOfRange;
+        }
+    };
+    auto loaded = [&]() {
+        xbase += xstep;
+        ybase += ystep;
+        if (--left == 0) {
+            if (STREAM) next_load();
+            else nothing();
+        }
+    };
+
+    // ---- fragments and products
+    const Fragments<TY, XC, TM, MB> xfrag(lane, wm * MB);
+    const Fragments<TY, YC, TN, NB> yfrag(lane, wn * NB);
+    i32x4_t f[4][NR];                            // f[step][X blocks, then Y blocks]
+    auto read_frag = [&](int kk, int i, uint32_t so) {
+        f[kk][i] = i < MB ? xfrag.read(smem, so, i, kk) : yfrag.read(smem + X_BYTES, so, i - MB, kk);
+    };
+    Acc<TY> acc[NB][MB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) acc[nb][mb] = zero_acc<TY>();
+    auto mul = [&](int kk, int q) { multiply<TY>(f[kk][MB + q / MB], f[kk][q % MB], acc[q / MB][q % MB]); };
+
+    // the refilling loads go out over SLOTS MFMAs: those of step 1 after FREE,
+    // and steps 2 and 3
+    constexpr int FREE = NM >= 4 ? NM * 3 / 4 : NM;
+    constexpr int SLOTS = NM - FREE + 2 * NM;
+    constexpr int BEFORE3 = (SLOTS - NM) * NL / SLOTS;
+    constexpr int RD3 = NM >= 2 ? NM / 2 : 1;    // MFMAs of step 1 that read step 3's fragments
+    // stores of an epilogue (always all of them: lanes without an output are
+    // out of range), which stand between the loads that the first wait after
+    // it is for and the later ones (float32: more than the counter holds, so
+    // that wait is for the stores too)
+    constexpr int STORES = BF_OUT ? MB * (NB / NP) * (32 / RPS) : 0;
+    // loads younger than the next slice's at the wait for it
+    constexpr int YOUNGER = (NS - 2) * NL + BEFORE3;
+    static_assert(YOUNGER + STORES < 64 && (NS - 1) * NL < 64, "vmcnt");
+    uint32_t so = 0;                             // the stage being multiplied
+    auto slice = [&](bool stored) {              // (stored: the first after an epilogue)
+        const uint32_t nso = so + STAGE == NS * STAGE ? 0 : so + STAGE;
+        auto refill = [&](int p) {
+#pragma unroll
+            for (int l = p * NL / SLOTS; l < (p + 1) * NL / SLOTS; ++l) dma(l, so);
+        };
+#pragma unroll
+        for (int q = 0; q < NM; ++q) {
+            mul(0, q);
+#pragma unroll
+            for (int i = q * 2 * NR / NM; i < (q + 1) * 2 * NR / NM; ++i) read_frag(1 + i / NR, i % NR, so);
             __builtin_amdgcn_sched_barrier(0);
         }
-        if (MORE) {
-            wait_vmcnt<BEFORE3>();
-            barrier_lds();
-        } else if (kt + 1 < nk) {
-            wait_vmcnt<0>();
-            barrier_lds();
+#pragma unroll
+        for (int q = 0; q < NM; ++q) {
+            mul(1, q);
+            if (q < RD3) {
+#pragma unroll
+                for (int i = q * NR / RD3; i < (q + 1) * NR / RD3; ++i) read_frag(3, i, so);
+            }
+            if (q >= FREE) refill(q - FREE);
+            __builtin_amdgcn_sched_barrier(0);
+            if (q == FREE - 1) {
+                wait_vmcnt_lgkm0<63>();
+                barrier_lds();
+                cut_tail();
+            }
         }
-        // (after the last slice this reads a stale stage whose values are
-        // never used)
+#pragma unroll
+        for (int q = 0; q < NM; ++q) {
+            mul(2, q);
+            refill(NM - FREE + q);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (STREAM && STORES > 0 && stored) wait_vmcnt<YOUNGER + STORES>();
+        else wait_vmcnt<YOUNGER>();
+        barrier_lds();
+        // (after the last slice of all this reads zeros that are never used)
 #pragma unroll
         for (int q = 0; q < NM; ++q) {
             mul(3, q);
-            if (MORE) {
-                refill(2 * NM + q, kt);
-                __builtin_amdgcn_sched_barrier(0);
-            }
+            refill(2 * NM - FREE + q);
 #pragma unroll
             for (int i = q * NR / NM; i < (q + 1) * NR / NM; ++i) read_frag(0, i, nso);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);
+        loaded();
+        so = nso;
     };
-    int kt = 0;
-    for (; kt + 2 < nk; ++kt) slice(kt, std::true_type{});
-    for (; kt < nk; ++kt) slice(kt, std::false_type{});
 
     // ---- epilogue
     // lane: output row m0 + (wm * MB + mb) * 32 + l32, columns p0 + (wn * NB +
     // nb) * 32 + 8 g + 4 half + 0..3 in registers 4 g .. 4 g + 3
-    float rs[MB];
-    if constexpr (TY == kI8) {
+    auto epilogue = [&](const Tile& t) {
+        int lane = tid & 63;
+        asm volatile("" : "+v"(lane));  // (as in aim)
+        const int half = lane >> 5, l32 = lane & 31;
+        if (!STREAM) {
+            wait_vmcnt_lgkm0<0>();
+            barrier_lds();
+        }
+        const int mrow = t.m0 + wm * MB * 32, pcol = t.p0 + wn * NB * 32;
+        float rs[MB];
+        if constexpr (TY == kI8) {
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb) rs[mb] = sx[min(mrow + mb * 32 + l32, t.m1 - 1)];
+        }
+        O* const out = C + (MODE == kTN ? static_cast<int64_t>(t.e) * N * K : 0) + static_cast<int64_t>(mrow) * P + pcol;
+        f32x4_t cs[TY == kI8 ? NB : 1][4];
+        if constexpr (TY == kI8) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int col = min(pcol + nb * 32 + 8 * g + 4 * half, P - 4);
+                    cs[nb][g] = *reinterpret_cast<const f32x4_t*>(sy + static_cast<int64_t>(t.e) * N + col);
+                }
+        }
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
-            const int m = m0 + (wm * MB + mb) * 32 + l32;
-            rs[mb] = m < m1 ? sx[m] : 0.f;
-        }
-    }
-    auto values = [&](int nb, int mb, int g, float* v) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = static_cast<float>(acc[nb][mb][4 * g + i]);
-        if constexpr (TY == kI8) {
-            const int col = p0 + (wn * NB + nb) * 32 + 8 * g + 4 * half;
-            f32x4_t s = {0.f, 0.f, 0.f, 0.f};
-            if (col < P) s = *reinterpret_cast<const f32x4_t*>(sy + static_cast<int64_t>(e) * N + col);
+            for (int n0 = 0; n0 < NB; n0 += NP) {
+                // (the accumulators leave their registers here, block by block:
+                // without this the compiler copies all of them at once)
+                if constexpr (STREAM) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = v[i] * rs[mb] * s[i];
+                    for (int nb = 0; nb < NP; ++nb) asm volatile("" : "+a"(acc[n0 + nb][mb]));
+                }
+#pragma unroll
+                for (int nb = 0; nb < NP; ++nb)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        f32x4_t v;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            v[i] = static_cast<float>(acc[n0 + nb][mb][4 * g + i]);
+                            if constexpr (TY == kI8) v[i] = v[i] * rs[mb] * cs[TY == kI8 ? n0 + nb : 0][g][i];
+                        }
+                        // staged in LDS by the wave for itself, 16-byte chunk ch of
+                        // row r at ch ^ (r mod CPR)
+                        char* const row = smem + EPI_AT + wave * EPI + l32 * EROW;
+                        if constexpr (BF_OUT)
+                            *reinterpret_cast<uint2*>(row + (((nb * 4 + g) ^ (l32 & (CPR - 1))) * 16) + half * 8) =
+                                make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+                        else
+                            *reinterpret_cast<f32x4_t*>(row + (((2 * g + half) ^ (l32 & (CPR - 1))) * 16)) = v;
+                    }
+                // zero for the next tile (while the staged values settle)
+                if constexpr (STREAM) {
+#pragma unroll
+                    for (int nb = 0; nb < NP; ++nb) {
+                        acc[n0 + nb][mb] = zero_acc<TY>();
+                        asm volatile("" : "+a"(acc[n0 + nb][mb]));
+                    }
+                }
+                // whole chunks, consecutive lanes on consecutive chunks of a row
+                u32x4_t v[32 / RPS];
+                uint32_t off[32 / RPS];
+#pragma unroll
+                for (int i = 0; i < 32 / RPS; ++i) {
+                    const int r = i * RPS + lane / CPR;
+                    v[i] = *reinterpret_cast<const u32x4_t*>(smem + EPI_AT + wave * EPI + r * EROW +
+                                                             (((lane % CPR) ^ (r & (CPR - 1))) * 16));
+                }
+                const uint64_t base =
+                    uniform64(reinterpret_cast<uint64_t>(out) +
+                              static_cast<uint64_t>((static_cast<int64_t>(mb) * 32 * P + n0 * 32) * sizeof(O)));
+                const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+                    reinterpret_cast<void*>(base), 0, static_cast<int>(kOutOfRange), static_cast<int>(kRsrcWord3));
+#pragma unroll
+                for (int i = 0; i < 32 / RPS; ++i) {
+                    const int r = i * RPS + lane / CPR;
+                    const int c = (lane % CPR) * (16 / static_cast<int>(sizeof(O)));
+                    off[i] = mrow + mb * 32 + r < t.m1 && pcol + n0 * 32 + c < P
+                                 ? (static_cast<uint32_t>(r) * static_cast<uint32_t>(P) + c) * static_cast<uint32_t>(sizeof(O))
+                                 : kOutOfRange;
+                }
+                // rows of whole 128-byte lines past the L2's lifetime (bf16, 16384 x
+                // 4864 x 128: 57 us, 61 through it); other rows' stores share
+                // lines, which the L2 has to put together (x 4904: 160 us past
+                // it, 67 through it)
+                if (P % (128 / static_cast<int>(sizeof(O))) == 0) {
+#pragma unroll
+                    for (int i = 0; i < 32 / RPS; ++i)
+                        __builtin_amdgcn_raw_buffer_store_b128(v[i], rsrc, off[i], 0, kNonTemporal);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32 / RPS; ++i) __builtin_amdgcn_raw_buffer_store_b128(v[i], rsrc, off[i], 0, 0);
+                }
+                if constexpr (STREAM) __builtin_amdgcn_sched_barrier(0);
+            }
         }
     };
-    O* const out = C + (MODE == kTN ? static_cast<int64_t>(e) * N * K : 0);
-    if constexpr (sizeof(O) == 4) {
+
+    // ---- the stream
+    next_load();
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
-            const int m = m0 + (wm * MB + mb) * 32 + l32;
-            float* const row = reinterpret_cast<float*>(out) + static_cast<int64_t>(m) * P;
+    for (int st = 0; st < NS; ++st) {
+        cut_tail();
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+        for (int l = 0; l < NL; ++l) dma(l, st * STAGE);
+        loaded();
+    }
+    wait_vmcnt<(NS - 1) * NL>();
+    barrier_lds();
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int col = p0 + (wn * NB + nb) * 32 + 8 * g + 4 * half;
-                    float v[4];
-                    values(nb, mb, g, v);
-                    if (m < m1 && col < P) *reinterpret_cast<f32x4_t*>(row + col) = f32x4_t{v[0], v[1], v[2], v[3]};
-                }
+    for (int i = 0; i < NR; ++i) read_frag(0, i, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    // (one flat loop over slices, with the tile's end inside: nested loops make
+    // the compiler move the accumulators between registers at every tile)
+    Tile t;
+    int tiles = 0, n;
+    auto next_tile = [&]() {
+        if (tiles == loading) return false;
+        const int* const r = ring + (tiles & 3) * 8;
+        const i32x4_t v = *reinterpret_cast<const i32x4_t*>(r);
+        n = __builtin_amdgcn_readfirstlane(r[4]);
+        t.e = __builtin_amdgcn_readfirstlane(v[0]);
+        t.m0 = __builtin_amdgcn_readfirstlane(v[1]);
+        t.m1 = __builtin_amdgcn_readfirstlane(v[2]);
+        t.p0 = __builtin_amdgcn_readfirstlane(v[3]);
+        ++tiles;
+        return true;
+    };
+    bool stored = false, more = next_tile();
+    while (more) {
+        slice(stored);
+        stored = false;
+        if (--n == 0) {
+            epilogue(t);
+            stored = true;
+            more = next_tile();
         }
+    }
+    wait_vmcnt<0>();  // (the last loads still write LDS)
+}
+
+// ---- the split kernel ---------------------------------------------------------------
+//
+// For problems of too few tiles to fill the card: a 32 MB x 32 NB output tile per
+// workgroup, its slices dealt to the 4 waves in turn.  Each wave multiplies its
+// own slices into a whole tile of its own, from a private ring of 2 LDS stages,
+// without a barrier: a tile kernel's wave of this size would wait at two
+// barriers for every slice of a few MFMAs.  At the end the 4 partial tiles are
+// added in the order of the waves.
+//
+// The fragments of a slice are read while those of the slice before are
+// multiplied, then its stage takes the loads of the slice after next.  Slices
+// past the end are loaded out of range (zeros, no traffic), so that the number
+// of loads in flight, and with it the waits, is constant.
+template <int TY, int MODE, int MB, int NB, typename O>
+__global__ __launch_bounds__(256) void grouped_split_kernel(
+    const void* __restrict__ Xp, const void* __restrict__ Yp, const int32_t* __restrict__ offsets, int E, int rows,
+    int N, int K, O* __restrict__ C, const float* __restrict__ sx, const float* __restrict__ sy, int parts) {
+    constexpr bool XC = MODE == kTN, YC = MODE != kNT;
+    static_assert(TY != kI8 || MODE == kNT, "int8: forward only");
+    constexpr int TM = 32 * MB, TN = 32 * NB;
+    using XS = Slice<TY, XC, TM>;
+    using YS = Slice<TY, YC, TN>;
+    constexpr int EB = XS::EB;
+    constexpr int QS = 128 / EB;
+    constexpr int X_BYTES = TM * 128;
+    constexpr int STAGE = (TM + TN) * 128;
+    constexpr int RING = 2 * STAGE;              // per wave
+    constexpr int PADC = TN + 4;                 // row length of a partial tile in LDS
+    static_assert(TM * PADC * 4 <= RING && sizeof(Queues) <= 4 * RING, "LDS");
+    using Val = std::conditional_t<TY == kI8, int, float>;
+    typedef Val val4_t __attribute__((ext_vector_type(4)));
+    __shared__ __attribute__((aligned(1024))) char smem[4 * RING];
+    Queues& queues = *reinterpret_cast<Queues*>(smem);
+
+    const int P = MODE == kNT ? N : K;
+    Tile t;
+    load_queues<MODE == kTN>(offsets, E, rows, TM, queues);
+    {
+        const int xcd = blockIdx.x % kXcds, place = blockIdx.x / kXcds;
+        if constexpr (MODE == kTN) {
+            if (weight_tile(queues, E, N, K, TM, TN, QS, parts, xcd, place, t) != kTile) return;
+        } else {
+            t.q0 = 0;
+            t.q1 = MODE == kNT ? K : N;
+            if (row_tile(queues, E, TM, TN, P, xcd, place, t) != kTile) return;
+        }
+    }
+    __syncthreads();  // every lookup is done before the loads overwrite the table
+
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t xrow = static_cast<int64_t>(MODE == kNT ? K : N) * EB;
+    const int64_t yrow = static_cast<int64_t>(K) * EB;
+    const int64_t xstep = XC ? QS * xrow : 128, ystep = YC ? QS * yrow : 128;
+    const int nk = (t.q1 - t.q0 + QS - 1) / QS;
+    const int qtail = t.q1 - t.q0 - (nk - 1) * QS;
+    const uint64_t xbase = uniform64(
+        reinterpret_cast<uint64_t>(Xp) +
+        static_cast<uint64_t>(XC ? t.q0 * xrow + static_cast<int64_t>(t.m0) * EB : t.m0 * xrow));
+    const uint64_t ybase = uniform64(
+        reinterpret_cast<uint64_t>(Yp) +
+        static_cast<uint64_t>(MODE == kTN   ? t.q0 * yrow + static_cast<int64_t>(t.p0) * EB
+                              : MODE == kNN ? static_cast<int64_t>(t.e) * N * yrow + static_cast<int64_t>(t.p0) * EB
+                                            : (static_cast<int64_t>(t.e) * N + t.p0) * yrow));
+    const uint32_t lds_w = __builtin_amdgcn_readfirstlane(lds_addr(smem)) + wave * RING;
+    char* const mine = smem + wave * RING;
+    uint32_t xoff[XS::LOADS], yoff[YS::LOADS], xtail = 0, ytail = 0;
+#pragma unroll
+    for (int j = 0; j < XS::LOADS; ++j) {
+        xoff[j] = XS::offset(j, lane, static_cast<uint32_t>(xrow), t.m1 - t.m0);
+        xtail |= (XS::beyond(j, lane, qtail) ? 1u : 0u) << j;
+    }
+#pragma unroll
+    for (int j = 0; j < YS::LOADS; ++j) {
+        yoff[j] = YS::offset(j, lane, static_cast<uint32_t>(yrow), P - t.p0);
+        ytail |= (YS::beyond(j, lane, qtail) ? 1u : 0u) << j;
+    }
+    const Fragments<TY, XC, TM, MB> xfrag(lane, 0);
+    const Fragments<TY, YC, TN, NB> yfrag(lane, 0);
+    Acc<TY> acc[NB][MB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) acc[nb][mb] = zero_acc<TY>();
+
+    // NX: the loads of X that have a row in range (the others' LDS rows keep
+    // what was there, and only rows of C that are not stored see it)
+    auto stream = [&](auto nx_c) {
+        constexpr int NX = decltype(nx_c)::value;
+        constexpr int NL = YS::LOADS + NX;
+        auto dma = [&](int kt, uint32_t st) {
+            // all lanes out of range past the end, in the last slice those beyond it
+            const uint32_t xo = kt >= nk ? ~0u : (kt == nk - 1 ? xtail : 0u);
+            const uint32_t yo = kt >= nk ? ~0u : (kt == nk - 1 ? ytail : 0u);
+#pragma unroll
+            for (int j = 0; j < YS::LOADS; ++j)
+                lds_dma16_b(ybase + kt * ystep, yoff[j] | ((yo << (31 - j)) & kOutOfRange), lds_w + st + X_BYTES + j * 1024);
+#pragma unroll
+            for (int j = 0; j < NX; ++j)
+                lds_dma16_b(xbase + kt * xstep, xoff[j] | ((xo << (31 - j)) & kOutOfRange), lds_w + st + j * 1024);
+        };
+        i32x4_t f[2][4][MB + NB];
+        auto read = [&](int b, uint32_t st) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+                for (int i = 0; i < MB; ++i) f[b][kk][i] = xfrag.read(mine, st, i, kk);
+#pragma unroll
+                for (int i = 0; i < NB; ++i) f[b][kk][MB + i] = yfrag.read(mine + X_BYTES, st, i, kk);
+            }
+        };
+        dma(wave, 0);
+        dma(wave + 4, STAGE);
+        wait_vmcnt<NL>();
+        read(0, 0);
+        wait_vmcnt_lgkm0<63>();
+        __builtin_amdgcn_sched_barrier(0);
+        dma(wave + 8, 0);
+        // two slices a round (the second possibly past the end: zeros)
+        for (int kt = wave; kt < nk; kt += 8) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const uint32_t st = u == 0 ? STAGE : 0;  // the stage of the slice after this one
+                wait_vmcnt<NL>();
+                asm volatile("" ::: "memory");
+                read(1 - u, st);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int mb = 0; mb < MB; ++mb) multiply<TY>(f[u][kk][MB + nb], f[u][kk][mb], acc[nb][mb]);
+                wait_vmcnt_lgkm0<63>();
+                __builtin_amdgcn_sched_barrier(0);
+                dma(kt + 4 * u + 12, st);
+            }
+        }
+        wait_vmcnt<0>();
+    };
+    if constexpr (!XC && MB == 1) {
+        const int nx = (t.m1 - t.m0 + 7) / 8;
+        if (nx == 1) stream(std::integral_constant<int, 1>{});
+        else if (nx == 2) stream(std::integral_constant<int, 2>{});
+        else stream(std::integral_constant<int, 4>{});
     } else {
-        // bf16: each wave stages its own part of the tile in LDS (16-byte chunk
-        // ch of row r at ch ^ (r mod CPR)) and writes whole chunks, consecutive
-        // lanes on consecutive chunks of a row: full 128-byte lines
-        constexpr int CPR = NB * 4;
-        constexpr int ROWO = NB * 64;
-        static_assert(4 * MB * 32 * ROWO <= 2 * STAGE, "the staged tile must fit the stages");
-        wait_vmcnt_lgkm0<0>();
-        barrier_lds();
-        char* const st = smem + wave * (MB * 32 * ROWO);
+        stream(std::integral_constant<int, XS::LOADS>{});
+    }
+
+    // the waves' partial tiles side by side, each in its wave's ring
+    {
+        const int half = lane >> 5, l32 = lane & 31;
+        Val* const part = reinterpret_cast<Val*>(mine);
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
-            const int r = mb * 32 + l32;
+        for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    float v[4];
-                    values(nb, mb, g, v);
-                    *reinterpret_cast<uint2*>(st + r * ROWO + (((nb * 4 + g) ^ (r & (CPR - 1))) * 16) + half * 8) =
-                        make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-                }
+                for (int g = 0; g < 4; ++g)
+                    *reinterpret_cast<val4_t*>(part + (mb * 32 + l32) * PADC + nb * 32 + 8 * g + 4 * half) =
+                        val4_t{acc[nb][mb][4 * g], acc[nb][mb][4 * g + 1], acc[nb][mb][4 * g + 2], acc[nb][mb][4 * g + 3]};
+    }
+    __syncthreads();
+#pragma unroll
+    for (int it = 0; it < TM * TN / 1024; ++it) {
+        const int idx = it * 256 + tid;
+        const int r = idx / (TN / 4), c = idx % (TN / 4) * 4;
+        const int m = t.m0 + r, col = t.p0 + c;
+        if (m >= t.m1 || col >= P) continue;
+        const char* const src = smem + (r * PADC + c) * 4;
+        val4_t v = *reinterpret_cast<const val4_t*>(src);
+#pragma unroll
+        for (int w = 1; w < 4; ++w) v += *reinterpret_cast<const val4_t*>(src + w * RING);
+        f32x4_t o;
+        if constexpr (TY == kI8) {
+            const float rs = sx[m];
+            const f32x4_t cs = *reinterpret_cast<const f32x4_t*>(sy + static_cast<int64_t>(t.e) * N + col);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = static_cast<float>(v[i]) * rs * cs[i];
+        } else {
+            o = v;
         }
-#pragma unroll 4
-        for (int idx = lane; idx < MB * 32 * CPR; idx += 64) {
-            const int r = idx / CPR, ch = idx % CPR;
-            const int m = m0 + wm * MB * 32 + r;
-            const int col = p0 + wn * NB * 32 + ch * 8;
-            if (m >= m1 || col >= P) continue;
-            const u32x4_t v = *reinterpret_cast<const u32x4_t*>(st + r * ROWO + ((ch ^ (r & (CPR - 1))) * 16));
-            __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(reinterpret_cast<bf16_t*>(out) + static_cast<int64_t>(m) * P + col));
-        }
+        O* const dst = C + (MODE == kTN ? static_cast<int64_t>(t.e) * N * K : 0) + static_cast<int64_t>(m) * P + col;
+        if constexpr (sizeof(O) == 4) *reinterpret_cast<f32x4_t*>(dst) = o;
+        else *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
     }
 }
 
+// Sums of a cut weight gradient: dst[i] = sum of the parts, in their order.
+template <typename O>
+__global__ __launch_bounds__(256) void grouped_parts_kernel(const float* __restrict__ src, int64_t n, int parts,
+                                                            O* __restrict__ dst) {
+    const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    f32x4_t v = *reinterpret_cast<const f32x4_t*>(src + i);
+    for (int p = 1; p < parts; ++p) v += *reinterpret_cast<const f32x4_t*>(src + p * n + i);
+    if constexpr (sizeof(O) == 4) *reinterpret_cast<f32x4_t*>(dst + i) = v;
+    else *reinterpret_cast<uint2*>(dst + i) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
+
+// ---- which kernel -------------------------------------------------------------------
+
+// Row tiles of bm rows that any queues of `rows` rows can have: each queue
+// that is not empty ends in at most one partial tile.
+int64_t row_tiles(const moe_grouped_t& g, int bm) {
+    return (g.rows + (bm - 1) * std::min<int64_t>(g.E, g.rows)) / bm;
+}
+
+// The kernels and their tiles (rows x columns).
+enum Variant { kSplit32, kSplit64, kTile64, kTile64x128, kTile128, kTile256, kVariants };
+constexpr int kTileM[kVariants] = {32, 64, 64, 64, 128, 256};
+constexpr int kTileN[kVariants] = {32, 64, 64, 128, 128, 256};
+
+// What a round of one tile per CU takes, in 10 ns: for every slice, and once
+// (start, epilogue), and no less than its stores.  Fitted to sweeps of rows,
+// queues and widths (E 1 to 128, rows per queue 1 to 1024, widths 768 to 4096);
+// on random problems the choice is within 5 % of the best variant in the mean.
+// A tile of a quarter the size takes more than a quarter of the time, so the
+// choice is between filling the last round and the rate within a round.  Both
+// sides, bf16: 8 queues of 512 rows, 4096 x 2048, tiles of 128 in 5 rounds 92 us,
+// tiles of 256 in 2 rounds 101 us; 64 queues of 512, 1408 x 2048, 13 rounds of
+// 128 243 us, 4 rounds of 256 224 us; one queue of 128 rows, 4096 x 4096, split
+// tiles of 32 in 2 rounds 16 us, tiles of 128 in one round 33 us.
+struct Cost {
+    int slice, once;
+};
+constexpr Cost kCost16[kVariants] = {{9, 100}, {25, 300}, {0, 0}, {30, 200}, {48, 170}, {148, 400}};
+// float32 is bound by its matrix instructions: 64 x 64 tiles are as fast per
+// output as larger ones.
+constexpr Cost kCost32[kVariants] = {{17, 130}, {0, 0}, {50, 20}, {0, 0}, {0, 0}, {0, 0}};
+// Weight gradients of short queues are bound by their stores and starts (128
+// queues of 32 rows, 768 x 2048: float32 tiles of 64 516 us, of 128 374 us; bf16
+// tiles of 128 199 us, of 256 88 us).
+constexpr Cost kCostW16[kVariants] = {{0, 0}, {0, 0}, {0, 0}, {0, 0}, {53, 350}, {150, 500}};
+constexpr Cost kCostW32[kVariants] = {{0, 0}, {0, 0}, {50, 150}, {0, 0}, {195, 330}, {800, 600}};
+constexpr int kCus = 256;
+constexpr int kMaxParts = 32;
+
+// What each mode and type has.
+bool has(Variant v, int mode, bool f32) {
+    if (mode == kTN) return v == kTile128 || v == kTile256 || (f32 && v == kTile64);
+    return f32 ? v == kSplit32 || v == kTile64 : v != kTile64;
+}
+
+struct Plan {
+    Variant v;
+    int parts;      // kTN: ranges each queue is cut into
+    int64_t tiles;  // at most
+};
+
+// The cheapest variant for mode `mode` of problem g.  The host knows the queues'
+// number and sum only: a queue is taken to end in half a tile.
+Plan plan_for(const moe_grouped_t& g, int mode, bool int8) {
+    const bool f32 = g.dtype == MOE_DTYPE_F32 && !int8;
+    const Cost* const cost = mode == kTN ? (f32 ? kCostW32 : kCostW16) : (f32 ? kCost32 : kCost16);
+    const int64_t M = g.N, P = mode == kNT ? g.N : g.K;
+    const int64_t qs = int8 ? 128 : (f32 ? 32 : 64);
+    const int64_t live = std::max<int64_t>(std::min<int64_t>(g.E, g.rows), 1);
+    Plan best{kTile128, 1, 0};
+    double least = 0;
+    // a round's stores at 5.5 TB/s
+    auto round_time = [&](int v, int64_t n, int bytes) {
+        const double stores = 100.0 * kCus * kTileM[v] * kTileN[v] * bytes / 5.5e6;
+        return std::max(static_cast<double>(cost[v].once + cost[v].slice * n), stores);
+    };
+    const int out_bytes = g.dtype == MOE_DTYPE_BF16 ? 2 : 4;
+    for (int i = 0; i < kVariants; ++i) {
+        const Variant v = static_cast<Variant>(i);
+        if (!has(v, mode, f32)) continue;
+        const int64_t pt = ceil_div(P, kTileN[v]);
+        if (mode == kTN) {
+            const int64_t whole = g.E * ceil_div(M, kTileM[v]) * pt;
+            const int64_t n = std::max<int64_t>(ceil_div(ceil_div(g.rows, live), qs), 1);
+            for (int parts = 1; parts <= kMaxParts && (parts == 1 || n >= 4 * parts); ++parts) {
+                const int64_t rounds = ceil_div(whole * parts, kCus);
+                double t = static_cast<double>(rounds) * round_time(v, ceil_div(n, parts), parts > 1 ? 4 : out_bytes);
+                // the operands into the XCDs' L2s at 8 TB/s: each into one when whole
+                // (parts of) queues are dealt, else into every XCD whose eighth
+                // of the tiles needs it
+                const int64_t mtn = ceil_div(M, kTileM[v]), per_x = ceil_div(mtn * pt, kXcds);
+                const int64_t m_x = std::min(mtn, kGroupM * ceil_div(per_x, kGroupM * pt));
+                const int64_t p_x = std::min(pt, ceil_div(per_x, kGroupM));
+                const bool dealt = whole_queues(g.E * parts);
+                const double reads = static_cast<double>(g.rows) * (f32 ? 4 : 2) *
+                                     (g.N * (dealt ? 1.0 : static_cast<double>(kXcds * m_x) / mtn) +
+                                      g.K * (dealt ? 1.0 : static_cast<double>(kXcds * p_x) / pt));
+                t = std::max(t, 100.0 * reads / 8e6);
+                // (a launch of the largest tiles takes longer to start)
+                if (v == kTile256) t += 500;
+                // the parts' sums written, read and added (4 TB/s), and a launch
+                if (parts > 1)
+                    t += 300 + 100.0 * (parts * 8.0 + 4.0) * static_cast<double>(g.E) * g.N * g.K / 4e6;
+                if (least == 0 || t < least) {
+                    least = t;
+                    best = Plan{v, parts, whole * parts};
+                }
+            }
+        } else {
+            const int64_t n = ceil_div(mode == kNT ? g.K : g.N, qs);
+            // row tiles: a queue's last one is half full in the mean, and their
+            // number varies by sqrt(live / 12); rounds: the mean over that spread
+            const double mt = static_cast<double>(g.rows) / kTileM[v] + 0.5 * live;
+            const double spread = std::sqrt(live / 12.0);
+            const double low = std::max<double>(live, mt - spread), high = std::max<double>(live, mt + spread);
+            const double rounds = 0.5 * (std::ceil(low * pt / kCus) + std::ceil(high * pt / kCus));
+            const double t = rounds * round_time(v, n, out_bytes);
+            if (least == 0 || t < least) {
+                least = t;
+                best = Plan{v, 1, row_tiles(g, kTileM[v]) * pt};
+            }
+        }
+    }
+    return best;
+}
+
+size_t parts_bytes(const moe_grouped_t& g, const Plan& p) {
+    return p.parts > 1 ? static_cast<size_t>(p.parts) * g.E * g.N * g.K * 4 : 0;
+}
+
+// CUs of the device of stream s.
+int compute_units(hipStream_t s) {
+    hipDevice_t dev = 0;
+    int cus = 0;
+    if (hipStreamGetDevice(s, &dev) != hipSuccess ||
+        hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
+        return kCus;
+    return cus;
+}
+
+struct Args {
+    const moe_grouped_t& g;
+    const void* X;
+    const void* Y;
+    const int32_t* offsets;
+    const float* sx;
+    const float* sy;
+    hipStream_t s;
+};
+
+template <int TY, int MODE, int MB, int NB, int NS, typename O>
+void start_tile(const Args& a, const Plan& p, unsigned grid, O* C) {
+    grouped_tile_kernel<TY, MODE, MB, NB, NS, O><<<grid, 256, 0, a.s>>>(
+        a.X, a.Y, a.offsets, a.g.E, static_cast<int>(a.g.rows), a.g.N, a.g.K, C, a.sx, a.sy, p.parts);
+}
 template <int TY, int MODE, int MB, int NB, typename O>
-hipError_t launch_tile(const moe_grouped_t& g, const void* X, const void* Y, const int32_t* offsets, void* C,
-                       const float* sx, const float* sy, hipStream_t s) {
-    const int tm = 64 * MB, tn = 64 * NB;
-    int64_t grid;
-    if (MODE == kTN)
-        grid = g.E * ceil_div(g.N, tm) * ceil_div(g.K, tn);
-    else
-        grid = static_cast<int64_t>(align_up(max_m_tiles(g.rows, g.E, tm) * ceil_div(MODE == kNT ? g.N : g.K, tn), kXcds));
-    grouped_tile_kernel<TY, MODE, MB, NB, O><<<static_cast<unsigned>(grid), 256, 0, s>>>(
-        X, Y, offsets, g.E, static_cast<int>(g.rows), g.N, g.K, static_cast<O*>(C), sx, sy);
-    return hipGetLastError();
+void start_split(const Args& a, const Plan& p, unsigned grid, O* C) {
+    grouped_split_kernel<TY, MODE, MB, NB, O><<<grid, 256, 0, a.s>>>(
+        a.X, a.Y, a.offsets, a.g.E, static_cast<int>(a.g.rows), a.g.N, a.g.K, C, a.sx, a.sy, p.parts);
 }
 
 template <int TY, int MODE, typename O>
-hipError_t launch(const moe_grouped_t& g, const void* X, const void* Y, const int32_t* offsets, void* C,
-                  const float* sx, const float* sy, hipStream_t s) {
-    const int64_t P = MODE == kNT ? g.N : g.K;
-    if constexpr (TY != kF32) {
-        const int64_t tiles = MODE == kTN ? g.E * ceil_div(g.N, 256) * ceil_div(P, 256)
-                                          : ceil_div(g.rows, 256) * ceil_div(P, 256);
-        if (tiles >= 256 && (MODE == kTN || g.rows >= 128 * static_cast<int64_t>(g.E)))
-            return launch_tile<TY, MODE, 4, 4, O>(g, X, Y, offsets, C, sx, sy, s);
+hipError_t start(const Args& a, const Plan& p, void* out) {
+    O* const C = static_cast<O*>(out);
+    const moe_grouped_t& g = a.g;
+    int64_t n = static_cast<int64_t>(align_up(p.tiles, kXcds));
+    if (MODE == kTN) {
+        // (every XCD's list is sized for the most tiles one XCD receives)
+        const int64_t queues = static_cast<int64_t>(g.E) * p.parts, whole = p.tiles / queues;
+        n = kXcds * (whole_queues(queues) ? ceil_div(queues, kXcds) * whole : g.E * ceil_div(whole * p.parts, kXcds));
     }
-    if (MODE != kTN && g.rows < 64 * static_cast<int64_t>(g.E))
-        return launch_tile<TY, MODE, 1, 2, O>(g, X, Y, offsets, C, sx, sy, s);
-    return launch_tile<TY, MODE, 2, 2, O>(g, X, Y, offsets, C, sx, sy, s);
+    // the largest tiles leave room for one workgroup per CU: that many walk
+    // all tiles
+    if (p.v == kTile256) n = std::min<int64_t>(n, align_up(compute_units(a.s), kXcds));
+    const unsigned grid = static_cast<unsigned>(n);
+    if constexpr (MODE == kTN) {
+        if (p.v == kTile256) {
+            start_tile<TY, MODE, 4, 4, 2>(a, p, grid, C);
+        } else if (p.v == kTile64) {
+            if constexpr (TY == kF32) start_tile<TY, MODE, 1, 1, 2>(a, p, grid, C);
+        } else {
+            start_tile<TY, MODE, 2, 2, 2>(a, p, grid, C);
+        }
+    } else if constexpr (TY == kF32) {
+        if (p.v == kSplit32) start_split<TY, MODE, 1, 1>(a, p, grid, C);
+        else start_tile<TY, MODE, 1, 1, 2>(a, p, grid, C);
+    } else {
+        switch (p.v) {
+            case kSplit32: start_split<TY, MODE, 1, 1>(a, p, grid, C); break;
+            case kSplit64: start_split<TY, MODE, 2, 2>(a, p, grid, C); break;
+            case kTile64x128: start_tile<TY, MODE, 1, 2, 3>(a, p, grid, C); break;
+            case kTile256: start_tile<TY, MODE, 4, 4, 2>(a, p, grid, C); break;
+            default: start_tile<TY, MODE, 2, 2, 2>(a, p, grid, C); break;
+        }
+    }
+    return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t grouped_grid_bound(const moe_grouped_t& g) {
-    const int64_t n = ceil_div(g.N, 128), k = ceil_div(g.K, 128);
-    return std::max(max_m_tiles(g.rows, g.E, 64) * std::max(n, k) + kXcds, g.E * n * k);
+int64_t grouped_tiles(const moe_grouped_t& g, bool int8) {
+    int64_t n = plan_for(g, kNT, int8).tiles;
+    if (!int8) n = std::max({n, plan_for(g, kNN, false).tiles, plan_for(g, kTN, false).tiles});
+    return n;
 }
 
-size_t grouped_ws_bytes(const moe_grouped_t&, int) { return 0; }
+size_t grouped_ws_bytes(const moe_grouped_t& g, int op) {
+    return op == MOE_GROUPED_OP_BACKWARD ? parts_bytes(g, plan_for(g, kTN, false)) : 0;
+}
 
 hipError_t launch_grouped_matmul(const moe_grouped_t& g, const void* a, const void* w, const int32_t* offsets, void* c,
-                                 void*, hipStream_t s) {
-    if (g.dtype == MOE_DTYPE_BF16) return launch<kBf16, kNT, bf16_t>(g, a, w, offsets, c, nullptr, nullptr, s);
-    return launch<kF32, kNT, float>(g, a, w, offsets, c, nullptr, nullptr, s);
+                                 hipStream_t s) {
+    const Args args{g, a, w, offsets, nullptr, nullptr, s};
+    const Plan p = plan_for(g, kNT, false);
+    return g.dtype == MOE_DTYPE_BF16 ? start<kBf16, kNT, bf16_t>(args, p, c) : start<kF32, kNT, float>(args, p, c);
 }
 
 hipError_t launch_grouped_da(const moe_grouped_t& g, const void* dc, const void* w, const int32_t* offsets, void* da,
-                             void*, hipStream_t s) {
-    if (g.dtype == MOE_DTYPE_BF16) return launch<kBf16, kNN, bf16_t>(g, dc, w, offsets, da, nullptr, nullptr, s);
-    return launch<kF32, kNN, float>(g, dc, w, offsets, da, nullptr, nullptr, s);
+                             hipStream_t s) {
+    const Args args{g, dc, w, offsets, nullptr, nullptr, s};
+    const Plan p = plan_for(g, kNN, false);
+    return g.dtype == MOE_DTYPE_BF16 ? start<kBf16, kNN, bf16_t>(args, p, da) : start<kF32, kNN, float>(args, p, da);
 }
 
 hipError_t launch_grouped_dw(const moe_grouped_t& g, const void* dc, const void* a, const int32_t* offsets, void* dw,
-                             void*, hipStream_t s) {
-    if (g.dtype == MOE_DTYPE_BF16) return launch<kBf16, kTN, bf16_t>(g, dc, a, offsets, dw, nullptr, nullptr, s);
-    return launch<kF32, kTN, float>(g, dc, a, offsets, dw, nullptr, nullptr, s);
+                             void* ws, hipStream_t s) {
+    const Args args{g, dc, a, offsets, nullptr, nullptr, s};
+    const Plan p = plan_for(g, kTN, false);
+    const bool bf16 = g.dtype == MOE_DTYPE_BF16;
+    if (p.parts == 1) return bf16 ? start<kBf16, kTN, bf16_t>(args, p, dw) : start<kF32, kTN, float>(args, p, dw);
+    const hipError_t e = bf16 ? start<kBf16, kTN, float>(args, p, ws) : start<kF32, kTN, float>(args, p, ws);
+    if (e != hipSuccess) return e;
+    const int64_t n = static_cast<int64_t>(g.E) * g.N * g.K;  // (a multiple of 16)
+    const unsigned grid = static_cast<unsigned>(ceil_div(n, 1024));
+    const float* const sums = static_cast<const float*>(ws);
+    if (bf16) grouped_parts_kernel<<<grid, 256, 0, s>>>(sums, n, p.parts, static_cast<bf16_t*>(dw));
+    else grouped_parts_kernel<<<grid, 256, 0, s>>>(sums, n, p.parts, static_cast<float*>(dw));
+    return hipGetLastError();
 }
 
 hipError_t launch_grouped_int8(const moe_grouped_t& g, const void* a, const float* sa, const void* w, const float* sw,
-                               const int32_t* offsets, void* c, void*, hipStream_t s) {
-    if (g.dtype == MOE_DTYPE_BF16) return launch<kI8, kNT, bf16_t>(g, a, w, offsets, c, sa, sw, s);
-    return launch<kI8, kNT, float>(g, a, w, offsets, c, sa, sw, s);
+                               const int32_t* offsets, void* c, hipStream_t s) {
+    const Args args{g, a, w, offsets, sa, sw, s};
+    const Plan p = plan_for(g, kNT, true);
+    return g.dtype == MOE_DTYPE_BF16 ? start<kI8, kNT, bf16_t>(args, p, c) : start<kI8, kNT, float>(args, p, c);
 }
 
 }  // namespace moe

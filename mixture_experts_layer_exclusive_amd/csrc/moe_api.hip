@@ -169,7 +169,8 @@ moe_status_t check_grouped(const moe_grouped_t* g, bool int8) {
     if (g == nullptr) return MOE_ERR_INVALID_ARGUMENT;
     if (g->rows < 0 || g->E < 1 || g->N < 1 || g->K < 1) return MOE_ERR_INVALID_ARGUMENT;
     if (g->dtype != MOE_DTYPE_F32 && g->dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARGUMENT;
-    if (g->E > MOE_MAX_EXPERTS || g->rows > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    // (row numbers past a matrix's end, by less than a tile, stay within int32)
+    if (g->E > MOE_MAX_EXPERTS || g->rows > INT32_MAX - 0xffff) return MOE_ERR_UNSUPPORTED;
     if (g->N > MOE_GROUPED_MAX_DIM || g->K > MOE_GROUPED_MAX_DIM) return MOE_ERR_UNSUPPORTED;
     if (int8) {
         // (int32 sums of products of at most 2^14: K < 2^17)
@@ -178,7 +179,8 @@ moe_status_t check_grouped(const moe_grouped_t* g, bool int8) {
         const int words = g->dtype == MOE_DTYPE_BF16 ? 8 : 4;
         if (g->K % words != 0 || g->N % words != 0) return MOE_ERR_UNSUPPORTED;
     }
-    if (grouped_grid_bound(*g) >= kMaxLaunchItems / 256) return MOE_ERR_UNSUPPORTED;
+    if (grouped_tiles(*g, int8) >= (1 << 24) - 8 * MOE_MAX_EXPERTS) return MOE_ERR_UNSUPPORTED;
+    if (!int8 && ceil_div(static_cast<int64_t>(g->E) * g->N * g->K, 1024) > kMaxLaunchItems / 256) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 
@@ -634,7 +636,7 @@ moe_status_t moe_grouped_matmul(const moe_grouped_t* g, const void* a, const voi
     MOE_TRY(need(c));
     MOE_TRY(need_grouped_ws(*g, MOE_GROUPED_OP_MATMUL, ws, ws_bytes));
     clear_hip_error();
-    MOE_LAUNCH(launch_grouped_matmul(*g, a, w, offsets, c, ws, static_cast<hipStream_t>(stream)));
+    MOE_LAUNCH(launch_grouped_matmul(*g, a, w, offsets, c, static_cast<hipStream_t>(stream)));
     return MOE_OK;
 }
 
@@ -654,7 +656,7 @@ moe_status_t moe_grouped_matmul_backward(const moe_grouped_t* g, const void* a, 
     MOE_TRY(need_grouped_ws(*g, MOE_GROUPED_OP_BACKWARD, ws, ws_bytes));
     hipStream_t s = static_cast<hipStream_t>(stream);
     clear_hip_error();
-    if (da != nullptr && g->rows > 0) MOE_LAUNCH(launch_grouped_da(*g, dc, w, offsets, da, ws, s));
+    if (da != nullptr && g->rows > 0) MOE_LAUNCH(launch_grouped_da(*g, dc, w, offsets, da, s));
     if (dw != nullptr) MOE_LAUNCH(launch_grouped_dw(*g, dc, a, offsets, dw, ws, s));
     return MOE_OK;
 }
@@ -688,7 +690,7 @@ moe_status_t moe_grouped_matmul_int8(const moe_grouped_t* g, const void* a, cons
     MOE_TRY(need(c));
     MOE_TRY(need_grouped_ws(*g, MOE_GROUPED_OP_INT8, ws, ws_bytes));
     clear_hip_error();
-    MOE_LAUNCH(launch_grouped_int8(*g, a, a_scales, w, w_scales, offsets, c, ws, static_cast<hipStream_t>(stream)));
+    MOE_LAUNCH(launch_grouped_int8(*g, a, a_scales, w, w_scales, offsets, c, static_cast<hipStream_t>(stream)));
     return MOE_OK;
 }
 

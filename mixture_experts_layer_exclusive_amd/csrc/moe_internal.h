@@ -159,19 +159,19 @@ hipError_t launch_backward_wgrad(const moe_problem_t& p, const void* A, int lda,
 
 // ---- grouped products -------------------------------------------------------
 
-// Largest 1-D grid, in 256-thread workgroups, a grouped product launches for
-// problem g, and the workspace of each (a moe_grouped_op_t value).
-int64_t grouped_grid_bound(const moe_grouped_t& g);
+// The most output tiles any of problem g's products has, and the workspace of
+// each (a moe_grouped_op_t value).
+int64_t grouped_tiles(const moe_grouped_t& g, bool int8);
 size_t grouped_ws_bytes(const moe_grouped_t& g, int op);
 
 hipError_t launch_grouped_matmul(const moe_grouped_t& g, const void* a, const void* w, const int32_t* offsets, void* c,
-                                 void* ws, hipStream_t s);
+                                 hipStream_t s);
 hipError_t launch_grouped_da(const moe_grouped_t& g, const void* dc, const void* w, const int32_t* offsets, void* da,
-                             void* ws, hipStream_t s);
+                             hipStream_t s);
 hipError_t launch_grouped_dw(const moe_grouped_t& g, const void* dc, const void* a, const int32_t* offsets, void* dw,
                              void* ws, hipStream_t s);
 hipError_t launch_grouped_int8(const moe_grouped_t& g, const void* a, const float* a_scales, const void* w,
-                               const float* w_scales, const int32_t* offsets, void* c, void* ws, hipStream_t s);
+                               const float* w_scales, const int32_t* offsets, void* c, hipStream_t s);
 hipError_t launch_quant_rows_int8(const void* src, int64_t rows, int cols, int dtype, void* codes, float* scales,
                                   hipStream_t s);
 
