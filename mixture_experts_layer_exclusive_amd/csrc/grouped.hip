@@ -694,7 +694,7 @@ Plan plan_for(const moe_grouped_t& g, int mode, bool int8) {
         if (mode == kTN) {
             const int64_t whole = g.E * ceil_div(M, kTileM[v]) * pt;
             const int64_t n = std::max<int64_t>(ceil_div(ceil_div(g.rows, live), qs), 1);
-            for (int parts = 1; parts <= kMaxParts && (parts == 1 || n >= 4 * parts); ++parts) {
+            for (int parts = 1; parts <= kMaxParts && (parts == 1 || (n >= 4 * parts && whole * parts <= 16 * kCus)); ++parts) {
                 const int64_t rounds = ceil_div(whole * parts, kCus);
                 double t = static_cast<double>(rounds) * round_time(v, ceil_div(n, parts), parts > 1 ? 4 : out_bytes);
                 // the operands into the XCDs' L2s at 8 TB/s: each into one when whole
@@ -810,10 +810,12 @@ hipError_t start(const Args& a, const Plan& p, void* out) {
 
 }  // namespace
 
-int64_t grouped_tiles(const moe_grouped_t& g, bool int8) {
-    int64_t n = plan_for(g, kNT, int8).tiles;
-    if (!int8) n = std::max({n, plan_for(g, kNN, false).tiles, plan_for(g, kTN, false).tiles});
-    return n;
+// (of the smallest tile each mode has; parts of queues are made only below 16
+// rounds)
+int64_t grouped_tiles(const moe_grouped_t& g) {
+    const int64_t widest = std::max(g.N, g.K);
+    return std::max(row_tiles(g, kTileM[kSplit32]) * ceil_div(widest, kTileN[kSplit32]),
+                    g.E * ceil_div(g.N, kTileM[kTile64]) * ceil_div(g.K, kTileN[kTile64]));
 }
 
 size_t grouped_ws_bytes(const moe_grouped_t& g, int op) {

@@ -179,7 +179,7 @@ moe_status_t check_grouped(const moe_grouped_t* g, bool int8) {
         const int words = g->dtype == MOE_DTYPE_BF16 ? 8 : 4;
         if (g->K % words != 0 || g->N % words != 0) return MOE_ERR_UNSUPPORTED;
     }
-    if (grouped_tiles(*g, int8) >= (1 << 24) - 8 * MOE_MAX_EXPERTS) return MOE_ERR_UNSUPPORTED;
+    if (grouped_tiles(*g) >= (1 << 24) - 8 * MOE_MAX_EXPERTS) return MOE_ERR_UNSUPPORTED;
     if (!int8 && ceil_div(static_cast<int64_t>(g->E) * g->N * g->K, 1024) > kMaxLaunchItems / 256) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }

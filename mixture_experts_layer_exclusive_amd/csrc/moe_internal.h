@@ -159,9 +159,9 @@ hipError_t launch_backward_wgrad(const moe_problem_t& p, const void* A, int lda,
 
 // ---- grouped products -------------------------------------------------------
 
-// The most output tiles any of problem g's products has, and the workspace of
-// each (a moe_grouped_op_t value).
-int64_t grouped_tiles(const moe_grouped_t& g, bool int8);
+// The most output tiles any of problem g's products can have, and the workspace
+// of each (a moe_grouped_op_t value).
+int64_t grouped_tiles(const moe_grouped_t& g);
 size_t grouped_ws_bytes(const moe_grouped_t& g, int op);
 
 hipError_t launch_grouped_matmul(const moe_grouped_t& g, const void* a, const void* w, const int32_t* offsets, void* c,
