@@ -37,8 +37,14 @@ namespace {
 // in step 0 would take longer than its MFMAs: 24 KB per wave at 128 bytes a
 // clock).  Then the stage is free, and the loads of the next-but-one slice go
 // out spread over the other MFMAs (an LDS-bound load holds up the MFMAs
-// behind it, so a burst of them stalls).  Before step 3 the next slice has
-// landed, and step 3 reads its first fragments.
+// behind it, so a burst of them stalls; the stream spreads them on over step 0
+// of the next slice: bf16, 8 x 2048 rows, 14336 x 4096, over 20 MFMAs 1643 us,
+// 28 1541, 36 1498, 52 1463).  Before step 3 the next slice has landed, and
+// step 3 reads its first fragments.
+//
+// The largest tiles at a long reduction are bound by power: the same product
+// over cached operands only, with one barrier per slice instead of two, or
+// with a part of its loads spread otherwise takes the same time to 1 %.
 template <int TY, int MODE, int MB, int NB, int NS, typename O>
 __global__ __launch_bounds__(256, (MB * NB > 4 ? 1 : 2)) void grouped_tile_kernel(
     const void* __restrict__ Xp, const void* __restrict__ Yp, const int32_t* __restrict__ offsets, int E, int rows,
@@ -207,36 +213,40 @@ __global__ __launch_bounds__(256, (MB * NB > 4 ? 1 : 2)) void grouped_tile_kerne
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) acc[nb][mb] = zero_acc<TY>();
-    auto mul = [&](int kk, int q) { multiply<TY>(f[kk][MB + q / MB], f[kk][q % MB], acc[q / MB][q % MB]); };
+    // (there and back over X, so that two products in a row share a fragment: 1 %)
+    auto mul = [&](int kk, int q) {
+        const int mb = q / MB % 2 ? MB - 1 - q % MB : q % MB;
+        multiply<TY>(f[kk][MB + q / MB], f[kk][mb], acc[q / MB][mb]);
+    };
 
     // the refilling loads go out over SLOTS MFMAs: those of step 1 after FREE,
-    // and steps 2 and 3
+    // steps 2 and 3, and LATE of the next slice's step 0
     constexpr int FREE = NM >= 4 ? NM * 3 / 4 : NM;
-    constexpr int SLOTS = NM - FREE + 2 * NM;
-    constexpr int BEFORE3 = (SLOTS - NM) * NL / SLOTS;
+    constexpr int LATE = STREAM ? NM : 0;
+    constexpr int SLOTS = NM - FREE + 2 * NM + LATE;
+    constexpr int BEFORE3 = (2 * NM - FREE) * NL / SLOTS;  // of them before step 3
+    constexpr int BEFORE0 = (SLOTS - LATE) * NL / SLOTS;   // before step 0
+    static_assert(LATE == 0 || NS == 2, "the late loads go into the other stage");
     constexpr int RD3 = NM >= 2 ? NM / 2 : 1;    // MFMAs of step 1 that read step 3's fragments
-    // stores of an epilogue (always all of them: lanes without an output are
-    // out of range), which stand between the loads that the first wait after
-    // it is for and the later ones (float32: more than the counter holds, so
-    // that wait is for the stores too)
-    constexpr int STORES = BF_OUT ? MB * (NB / NP) * (32 / RPS) : 0;
     // loads younger than the next slice's at the wait for it
     constexpr int YOUNGER = (NS - 2) * NL + BEFORE3;
-    static_assert(YOUNGER + STORES < 64 && (NS - 1) * NL < 64, "vmcnt");
+    static_assert((NS - 1) * NL < 64, "vmcnt");
     uint32_t so = 0;                             // the stage being multiplied
-    auto slice = [&](bool stored) {              // (stored: the first after an epilogue)
+    auto slice = [&]() {
         const uint32_t nso = so + STAGE == NS * STAGE ? 0 : so + STAGE;
-        auto refill = [&](int p) {
+        auto refill = [&](int p, uint32_t stage) {
 #pragma unroll
-            for (int l = p * NL / SLOTS; l < (p + 1) * NL / SLOTS; ++l) dma(l, so);
+            for (int l = p * NL / SLOTS; l < (p + 1) * NL / SLOTS; ++l) dma(l, stage);
         };
 #pragma unroll
         for (int q = 0; q < NM; ++q) {
             mul(0, q);
 #pragma unroll
             for (int i = q * 2 * NR / NM; i < (q + 1) * 2 * NR / NM; ++i) read_frag(1 + i / NR, i % NR, so);
+            if (q < LATE) refill(SLOTS - LATE + q, nso);
             __builtin_amdgcn_sched_barrier(0);
         }
+        if (LATE > 0) loaded();
 #pragma unroll
         for (int q = 0; q < NM; ++q) {
             mul(1, q);
@@ -244,7 +254,7 @@ __global__ __launch_bounds__(256, (MB * NB > 4 ? 1 : 2)) void grouped_tile_kerne
 #pragma unroll
                 for (int i = q * NR / RD3; i < (q + 1) * NR / RD3; ++i) read_frag(3, i, so);
             }
-            if (q >= FREE) refill(q - FREE);
+            if (q >= FREE) refill(q - FREE, so);
             __builtin_amdgcn_sched_barrier(0);
             if (q == FREE - 1) {
                 wait_vmcnt_lgkm0<63>();
@@ -255,22 +265,21 @@ __global__ __launch_bounds__(256, (MB * NB > 4 ? 1 : 2)) void grouped_tile_kerne
 #pragma unroll
         for (int q = 0; q < NM; ++q) {
             mul(2, q);
-            refill(NM - FREE + q);
+            refill(NM - FREE + q, so);
             __builtin_amdgcn_sched_barrier(0);
         }
-        if (STREAM && STORES > 0 && stored) wait_vmcnt<YOUNGER + STORES>();
-        else wait_vmcnt<YOUNGER>();
+        wait_vmcnt<YOUNGER>();
         barrier_lds();
         // (after the last slice of all this reads zeros that are never used)
 #pragma unroll
         for (int q = 0; q < NM; ++q) {
             mul(3, q);
-            refill(2 * NM - FREE + q);
+            refill(2 * NM - FREE + q, so);
 #pragma unroll
             for (int i = q * NR / NM; i < (q + 1) * NR / NM; ++i) read_frag(0, i, nso);
             __builtin_amdgcn_sched_barrier(0);
         }
-        loaded();
+        if (LATE == 0) loaded();
         so = nso;
     };
 
@@ -384,10 +393,10 @@ __global__ __launch_bounds__(256, (MB * NB > 4 ? 1 : 2)) void grouped_tile_kerne
     for (int st = 0; st < NS; ++st) {
         cut_tail();
 #pragma unroll
-        for (int l = 0; l < NL; ++l) dma(l, st * STAGE);
-        loaded();
+        for (int l = 0; l < (st < NS - 1 ? NL : BEFORE0); ++l) dma(l, st * STAGE);
+        if (LATE == 0 || st < NS - 1) loaded();
     }
-    wait_vmcnt<(NS - 1) * NL>();
+    wait_vmcnt<(NS - 2) * NL + BEFORE0>();
     barrier_lds();
 #pragma unroll
     for (int i = 0; i < NR; ++i) read_frag(0, i, 0);
@@ -408,13 +417,11 @@ __global__ __launch_bounds__(256, (MB * NB > 4 ? 1 : 2)) void grouped_tile_kerne
         ++tiles;
         return true;
     };
-    bool stored = false, more = next_tile();
+    bool more = next_tile();
     while (more) {
-        slice(stored);
-        stored = false;
+        slice();
         if (--n == 0) {
             epilogue(t);
-            stored = true;
             more = next_tile();
         }
     }
