@@ -210,6 +210,114 @@ def test_special_values_stay_in_their_rows(dtype, bad):
     assert torch.equal(d3[:, :, kc], g0["dw"][:, :, kc]) and not torch.isfinite(d3[[0, 1, 3], :, 5]).any()
 
 
+def ragged(total, E, seed):
+    """E queue lengths that sum to total: a third of the queues empty, the
+    others uneven, with a queue of one row."""
+    rng = np.random.default_rng(seed)
+    share = rng.random(E) ** 2 * (rng.random(E) > 1 / 3)
+    share[rng.integers(E)] = 1.0
+    counts = np.floor(share / share.sum() * total).astype(int)
+    counts[np.argmax(counts)] += total - counts.sum()
+    if E > 2 and (counts == 0).any():
+        counts[np.argmax(counts)] -= 1
+        counts[np.argmin(counts)] += 1
+    return [int(v) for v in counts]
+
+
+# Sizes at which the choice of the kernel falls on the less usual ones: the
+# 64 x 64 split tiles; the largest tiles as one stream of one, two, three and
+# many slices per tile, several tiles per workgroup; queues cut into parts.
+CHOICES = [
+    ("matmul", "bf16", 1370, 1, 496, 1744),
+    ("matmul", "bf16", 12626, 100, 464, 16),
+    ("matmul", "bf16", 5000, 3, 2056, 1160),
+    ("backward", "bf16", 1072, 8, 2704, 512),
+    ("backward", "bf16", 5241, 8, 176, 1728),
+    ("backward", "bf16", 8947, 40, 48, 3232),
+    ("backward", "bf16", 21678, 3, 1488, 144),
+    ("backward", "bf16", 35168, 5, 528, 336),
+    ("backward", "bf16", 3061, 16, 3600, 464),
+    ("backward", "f32", 3061, 16, 3600, 464),
+    ("backward", "f32", 13, 1, 3536, 4144),
+    ("backward", "f32", 15230, 3, 128, 1536),
+    ("backward", "f32", 10969, 3, 2608, 144),
+    ("int8", "bf16", 1427, 2, 480, 4176),
+    ("int8", "bf16", 9537, 8, 944, 32),
+    ("int8", "f32", 865, 3, 1008, 3920),
+    ("int8", "f32", 13787, 3, 592, 528),
+]
+
+
+@pytest.mark.parametrize("op,dtype,rows,E,N,K", CHOICES)
+def test_each_kernel(op, dtype, rows, E, N, K):
+    counts = ragged(rows, E, seed=rows)
+    assert sum(counts) == rows and min(counts) >= 0
+    what = f"{op} {rows} rows, {E} queues, {N}x{K}"
+    if op == "int8":
+        qa, sa, qw, sw, off = int8_case(16, counts, N, K)
+        t = lambda v: torch.from_numpy(v).to(DEV)  # noqa: E731
+        c = poisoned(rows, N, dtype=TORCH[dtype])
+        moe.grouped_matmul_int8(t(qa), t(sa), t(qw), t(sw), gpu_off(off), out_dtype=TORCH[dtype], c=c)
+        check_int8(c, G.matmul_int8(qa, sa, qw, sw, off), dtype, what)
+        return
+    off = offsets_of(counts)
+    a, w = normal(17, rows, K, dtype=dtype), normal(18, E, N, K, dtype=dtype)
+    if op == "matmul":
+        run_matmul(a, w, off, rows, N, dtype, what)
+    else:
+        run_backward(a, w, off, normal(19, rows, N, dtype=dtype), dtype, what)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_special_values_stay_in_their_rows_of_a_stream_of_tiles(bad):
+    """As above, at sizes where a workgroup goes from tile to tile: the rows
+    behind a queue, the end of the reduction and the next tile's first slice
+    lie in LDS beside one another."""
+    # forward: one quarter-full slice per tile
+    rows, E, N, K = 12626, 100, 464, 16
+    off = offsets_of(ragged(rows, E, seed=rows))
+    o = gpu_off(off)
+    a, w = normal(1, rows, K).to(DEV), normal(2, E, N, K).to(DEV)
+    e = int(np.argmax(np.diff(off)))
+    row = int(off[e]) + 3
+    c0 = moe.grouped_matmul(a, w, o)
+    a1, w1 = a.clone(), w.clone()
+    a1[row] = bad
+    c1 = moe.grouped_matmul(a1, w, o)
+    keep = torch.arange(rows, device=DEV) != row
+    assert torch.equal(c1[keep], c0[keep]) and not torch.isfinite(c1[row]).any()
+    w1[e] = bad
+    c2 = moe.grouped_matmul(a, w1, o)
+    keep = torch.ones(rows, dtype=torch.bool, device=DEV)
+    keep[int(off[e]):int(off[e + 1])] = False
+    assert torch.equal(c2[keep], c0[keep]) and not torch.isfinite(c2[~keep]).any()
+    # input gradient: three slices, the last not full
+    rows, E, N, K = 5241, 8, 176, 1728
+    off = offsets_of(ragged(rows, E, seed=rows))
+    o = gpu_off(off)
+    dc, w = normal(3, rows, N).to(DEV), normal(4, E, N, K).to(DEV)
+    e = int(np.argmax(np.diff(off)))
+    d0 = moe.grouped_matmul_backward(None, w, o, dc, with_dw=False)["da"]
+    w1 = w.clone()
+    w1[e] = bad
+    keep = torch.ones(rows, dtype=torch.bool, device=DEV)
+    keep[int(off[e]):int(off[e + 1])] = False
+    d1 = moe.grouped_matmul_backward(None, w1, o, dc, with_dw=False)["da"]
+    assert torch.equal(d1[keep], d0[keep]) and not torch.isfinite(d1[~keep]).any()
+    # weight gradient in parts: a row reaches its own expert only
+    rows, E, N, K = 21678, 3, 1488, 144
+    off = offsets_of([9000, 0, 12678])
+    o = gpu_off(off)
+    a, dc = normal(5, rows, K).to(DEV), normal(6, rows, N).to(DEV)
+    g0 = moe.grouped_matmul_backward(a, None, o, dc, with_da=False)["dw"]
+    for row, hit in ((8999, 0), (9000, 2)):
+        dc1 = dc.clone()
+        dc1[row] = bad
+        g1 = moe.grouped_matmul_backward(a, None, o, dc1, with_da=False)["dw"]
+        others = [i for i in range(E) if i != hit]
+        assert torch.equal(g1[others], g0[others]) and not torch.isfinite(g1[hit]).any()
+
+
 def test_offsets_outside_the_matrix_stay_inside_the_arrays():
     """Offsets that break the rules (beyond the rows, negative, descending)
     give unspecified values, but nothing outside the outputs is written."""
