@@ -374,11 +374,11 @@ moe_status_t moe_expert_ffn_fp8(const moe_problem_t* p, const void* x, const int
  * unspecified values in the outputs, never an access outside the arrays.
  *
  * Limits (MOE_ERR_UNSUPPORTED otherwise): 1 <= E <= MOE_MAX_EXPERTS;
- * 0 <= rows <= 2^31 - 1; N and K at most MOE_GROUPED_MAX_DIM; every matrix
+ * 0 <= rows <= 2^31 - 2^16; N and K at most MOE_GROUPED_MAX_DIM; every matrix
  * row a whole number of 16-byte words: N and K multiples of 8 (bf16) or of 4
- * (f32), for the 8-bit integer product K a multiple of 16 and N of 8; and a
- * launch of fewer than 2^24 workgroups (at least rows * N and E * N * K up
- * to 2^32 fit).  Outputs must not overlap the inputs.
+ * (f32), for the 8-bit integer product K a multiple of 16 and N of 8; and
+ * fewer than 2^24 - 2^11 output tiles (rows * max(N, K, 32) and E * N * K up
+ * to 2^32 always fit).  Outputs must not overlap the inputs.
  * Workspace: moe_grouped_workspace_size of the same problem; ws may be NULL
  * when that is 0.  No atomics: the same inputs give the same bits.
  */
