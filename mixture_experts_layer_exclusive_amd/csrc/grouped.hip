@@ -27,7 +27,7 @@ namespace {
 // two LDS stages.  The MFMA takes Y's fragment first and X's second, so a lane
 // holds one output row (lane & 31) and runs of 4 consecutive columns.
 //
-// A workgroup of the largest tiles walks its XCD's tiles in rounds of gridDim /
+// A workgroup of the largest tiles walks its XCD's tiles in rounds of blocks /
 // 8, and the slices of all its tiles are one stream: while a tile's last slices
 // are multiplied and its outputs stored, the first slices of the next are
 // landing.  (Weight gradients, whose tiles fall in cost: every other round is
@@ -48,10 +48,29 @@ namespace {
 // The largest tiles at a long reduction are bound by power: the same product
 // over cached operands only, with one barrier per slice instead of two, or
 // with a part of its loads spread otherwise takes the same time to 1 %.
+template <int MB, int NB, int NS, typename O>
+struct TileLds {
+    static constexpr int STAGE = 64 * (MB + NB) * 128;
+    static constexpr int NP = sizeof(O) == 2 && NB >= 2 ? 2 : 1;  // column blocks the epilogue stages at a time
+    static constexpr int EROW = NP * 32 * sizeof(O);  // bytes of a staged row: a 128-byte line (bf16, NB = 1: 64)
+    static constexpr int EPI = 32 * EROW;             // staged bytes per wave
+    // the largest tiles walk the tile order as one stream and stage their
+    // outputs beside the stages; the others take one tile and stage over them
+    static constexpr bool STREAM = MB * NB > 4;
+    static constexpr int EPI_AT = STREAM ? NS * STAGE : 0;
+    static constexpr int Q_AT = NS * STAGE + (STREAM ? 4 * EPI : 0);
+    static_assert(4 * EPI <= NS * STAGE, "the staged outputs must fit the stages");
+    static constexpr int BYTES = Q_AT + sizeof(Queues) + 512;
+    static_assert(BYTES <= 160 * 1024, "LDS");
+};
+
+// smem: TileLds::BYTES, 1024-byte aligned; workgroup `block` of `blocks`
 template <int TY, int MODE, int MB, int NB, int NS, typename O>
-__global__ __launch_bounds__(256, (MB * NB > 4 ? 1 : 2)) void grouped_tile_kernel(
-    const void* __restrict__ Xp, const void* __restrict__ Yp, const int32_t* __restrict__ offsets, int E, int rows,
-    int N, int K, O* __restrict__ C, const float* __restrict__ sx, const float* __restrict__ sy, int parts) {
+__device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block, int blocks, const void* __restrict__ Xp,
+                                             const void* __restrict__ Yp, const int32_t* __restrict__ offsets, int E,
+                                             int rows, int N, int K, O* __restrict__ C, const float* __restrict__ sx,
+                                             const float* __restrict__ sy, int parts) {
+    using Lds = TileLds<MB, NB, NS, O>;
     constexpr bool XC = MODE == kTN;             // X column-major
     constexpr bool YC = MODE != kNT;             // Y column-major
     static_assert(TY != kI8 || MODE == kNT, "int8: forward only");
@@ -63,23 +82,15 @@ __global__ __launch_bounds__(256, (MB * NB > 4 ? 1 : 2)) void grouped_tile_kerne
     constexpr int XL = XS::LOADS / 4, YL = YS::LOADS / 4;  // loads per wave and slice
     constexpr int NL = XL + YL;
     constexpr int X_BYTES = TM * 128;
-    constexpr int STAGE = (TM + TN) * 128;
+    constexpr int STAGE = Lds::STAGE;
     constexpr int NM = MB * NB;
     constexpr int NR = MB + NB;
     constexpr bool BF_OUT = sizeof(O) == 2;
-    constexpr int NP = BF_OUT && NB >= 2 ? 2 : 1;  // column blocks the epilogue stages at a time
-    constexpr int EROW = NP * 32 * sizeof(O);    // bytes of a staged row: a 128-byte line (bf16, NB = 1: 64)
+    constexpr int NP = Lds::NP, EROW = Lds::EROW, EPI = Lds::EPI;
     constexpr int CPR = EROW / 16;               // 16-byte chunks per staged row
     constexpr int RPS = 64 / CPR;                // rows per store
-    constexpr int EPI = 32 * EROW;               // staged bytes per wave
-    // the largest tiles walk the tile order as one stream and stage their
-    // outputs beside the stages; the others take one tile and stage over them
-    constexpr bool STREAM = NM > 4;
-    constexpr int EPI_AT = STREAM ? NS * STAGE : 0;
-    constexpr int Q_AT = NS * STAGE + (STREAM ? 4 * EPI : 0);
-    static_assert(4 * EPI <= NS * STAGE, "the staged outputs must fit the stages");
-    __shared__ __attribute__((aligned(1024))) char smem[Q_AT + sizeof(Queues) + 512];
-    static_assert(sizeof(smem) <= 160 * 1024, "LDS");
+    constexpr bool STREAM = Lds::STREAM;
+    constexpr int EPI_AT = Lds::EPI_AT, Q_AT = Lds::Q_AT;
     Queues& queues = *reinterpret_cast<Queues*>(smem + Q_AT);
 
     const int tid = threadIdx.x;
@@ -91,8 +102,8 @@ __global__ __launch_bounds__(256, (MB * NB > 4 ? 1 : 2)) void grouped_tile_kerne
     const int64_t yrow = static_cast<int64_t>(K) * EB;
 
     load_queues<MODE == kTN>(offsets, E, rows, TM, queues);
-    const int xcd = blockIdx.x % kXcds;
-    const int stride = gridDim.x / kXcds;
+    const int xcd = block % kXcds;
+    const int stride = blocks / kXcds;
     auto tile_at = [&](int place, Tile& t) -> Found {
         if constexpr (MODE == kTN) {
             return weight_tile(queues, E, N, K, TM, TN, QS, parts, xcd, place, t);
@@ -163,7 +174,7 @@ __global__ __launch_bounds__(256, (MB * NB > 4 ? 1 : 2)) void grouped_tile_kerne
     auto next_load = [&]() {
         for (;;) {
             Tile t;
-            const int at = blockIdx.x / kXcds;
+            const int at = block / kXcds;
             const Found f = tile_at(lround * stride + (MODE == kTN && (lround & 1) ? stride - 1 - at : at), t);
             ++lround;
             if (f == kTile) {
@@ -432,6 +443,14 @@ __global__ __launch_bounds__(256, (MB * NB > 4 ? 1 : 2)) void grouped_tile_kerne
     wait_vmcnt<0>();  // (the last loads still write LDS)
 }
 
+template <int TY, int MODE, int MB, int NB, int NS, typename O>
+__global__ __launch_bounds__(256, (MB * NB > 4 ? 1 : 2)) void grouped_tile_kernel(
+    const void* __restrict__ Xp, const void* __restrict__ Yp, const int32_t* __restrict__ offsets, int E, int rows,
+    int N, int K, O* __restrict__ C, const float* __restrict__ sx, const float* __restrict__ sy, int parts) {
+    __shared__ __attribute__((aligned(1024))) char smem[TileLds<MB, NB, NS, O>::BYTES];
+    grouped_tile<TY, MODE, MB, NB, NS, O>(smem, blockIdx.x, gridDim.x, Xp, Yp, offsets, E, rows, N, K, C, sx, sy, parts);
+}
+
 // ---- the split kernel ---------------------------------------------------------------
 //
 // For problems of too few tiles to fill the card: a 32 MB x 32 NB output tile per
@@ -445,10 +464,14 @@ __global__ __launch_bounds__(256, (MB * NB > 4 ? 1 : 2)) void grouped_tile_kerne
 // multiplied, then its stage takes the loads of the slice after next.  Slices
 // past the end are loaded out of range (zeros, no traffic), so that the number
 // of loads in flight, and with it the waits, is constant.
+constexpr int split_lds(int MB, int NB) { return 4 * 2 * (32 * MB + 32 * NB) * 128; }
+
+// smem: split_lds bytes, 1024-byte aligned
 template <int TY, int MODE, int MB, int NB, typename O>
-__global__ __launch_bounds__(256) void grouped_split_kernel(
-    const void* __restrict__ Xp, const void* __restrict__ Yp, const int32_t* __restrict__ offsets, int E, int rows,
-    int N, int K, O* __restrict__ C, const float* __restrict__ sx, const float* __restrict__ sy, int parts) {
+__device__ __forceinline__ void grouped_split(char* __restrict__ smem, int block, const void* __restrict__ Xp,
+                                              const void* __restrict__ Yp, const int32_t* __restrict__ offsets, int E,
+                                              int rows, int N, int K, O* __restrict__ C, const float* __restrict__ sx,
+                                              const float* __restrict__ sy, int parts) {
     constexpr bool XC = MODE == kTN, YC = MODE != kNT;
     static_assert(TY != kI8 || MODE == kNT, "int8: forward only");
     constexpr int TM = 32 * MB, TN = 32 * NB;
@@ -463,14 +486,14 @@ __global__ __launch_bounds__(256) void grouped_split_kernel(
     static_assert(TM * PADC * 4 <= RING && sizeof(Queues) <= 4 * RING, "LDS");
     using Val = std::conditional_t<TY == kI8, int, float>;
     typedef Val val4_t __attribute__((ext_vector_type(4)));
-    __shared__ __attribute__((aligned(1024))) char smem[4 * RING];
+    static_assert(4 * RING == split_lds(MB, NB), "LDS");
     Queues& queues = *reinterpret_cast<Queues*>(smem);
 
     const int P = MODE == kNT ? N : K;
     Tile t;
     load_queues<MODE == kTN>(offsets, E, rows, TM, queues);
     {
-        const int xcd = blockIdx.x % kXcds, place = blockIdx.x / kXcds;
+        const int xcd = block % kXcds, place = block / kXcds;
         if constexpr (MODE == kTN) {
             if (weight_tile(queues, E, N, K, TM, TN, QS, parts, xcd, place, t) != kTile) return;
         } else {
@@ -617,6 +640,41 @@ __global__ __launch_bounds__(256) void grouped_split_kernel(
         O* const dst = C + (MODE == kTN ? static_cast<int64_t>(t.e) * N * K : 0) + static_cast<int64_t>(m) * P + col;
         if constexpr (sizeof(O) == 4) *reinterpret_cast<f32x4_t*>(dst) = o;
         else *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+    }
+}
+
+template <int TY, int MODE, int MB, int NB, typename O>
+__global__ __launch_bounds__(256) void grouped_split_kernel(
+    const void* __restrict__ Xp, const void* __restrict__ Yp, const int32_t* __restrict__ offsets, int E, int rows,
+    int N, int K, O* __restrict__ C, const float* __restrict__ sx, const float* __restrict__ sy, int parts) {
+    __shared__ __attribute__((aligned(1024))) char smem[split_lds(MB, NB)];
+    grouped_split<TY, MODE, MB, NB, O>(smem, blockIdx.x, Xp, Yp, offsets, E, rows, N, K, C, sx, sy, parts);
+}
+
+// ---- both gradients in one launch -----------------------------------------------
+//
+// The input gradient's workgroups, then the weight gradient's: for problems of
+// a few rounds most of a kernel is its start and its last round, and the two
+// products fill each other's.
+// DMB = 0: the input gradient by the split kernel's 32 x 32 tiles.
+template <int TY, int DMB, int DNB, int DNS, int WMB, typename DO, typename WO>
+__global__ __launch_bounds__(256, 2) void grouped_gradients_kernel(
+    const void* __restrict__ dc, const void* __restrict__ w, const void* __restrict__ a,
+    const int32_t* __restrict__ offsets, int E, int rows, int N, int K, DO* __restrict__ da, WO* __restrict__ dw,
+    int da_blocks, int parts) {
+    constexpr int DA_LDS = DMB == 0 ? split_lds(1, 1) : TileLds<DMB == 0 ? 1 : DMB, DMB == 0 ? 1 : DNB, DNS, DO>::BYTES;
+    constexpr int DW_LDS = TileLds<WMB, WMB, 2, WO>::BYTES;
+    __shared__ __attribute__((aligned(1024))) char smem[DA_LDS > DW_LDS ? DA_LDS : DW_LDS];
+    const int block = blockIdx.x;
+    if (block < da_blocks) {
+        if constexpr (DMB == 0)
+            grouped_split<TY, kNN, 1, 1, DO>(smem, block, dc, w, offsets, E, rows, N, K, da, nullptr, nullptr, 1);
+        else
+            grouped_tile<TY, kNN, DMB, DNB, DNS, DO>(smem, block, da_blocks, dc, w, offsets, E, rows, N, K, da, nullptr,
+                                                     nullptr, 1);
+    } else {
+        grouped_tile<TY, kTN, WMB, WMB, 2, WO>(smem, block - da_blocks, gridDim.x - da_blocks, dc, a, offsets, E, rows,
+                                               N, K, dw, nullptr, nullptr, parts);
     }
 }
 
@@ -782,16 +840,18 @@ void start_split(const Args& a, const Plan& p, unsigned grid, O* C) {
         a.X, a.Y, a.offsets, a.g.E, static_cast<int>(a.g.rows), a.g.N, a.g.K, C, a.sx, a.sy, p.parts);
 }
 
+// Workgroups that plan p takes, one per tile: a multiple of 8.
+int64_t workgroups(const moe_grouped_t& g, int mode, const Plan& p) {
+    if (mode != kTN) return static_cast<int64_t>(align_up(p.tiles, kXcds));
+    // (every XCD's list is sized for the most tiles one XCD receives)
+    const int64_t queues = static_cast<int64_t>(g.E) * p.parts, whole = p.tiles / queues;
+    return kXcds * (whole_queues(queues) ? ceil_div(queues, kXcds) * whole : g.E * ceil_div(whole * p.parts, kXcds));
+}
+
 template <int TY, int MODE, typename O>
 hipError_t start(const Args& a, const Plan& p, void* out) {
     O* const C = static_cast<O*>(out);
-    const moe_grouped_t& g = a.g;
-    int64_t n = static_cast<int64_t>(align_up(p.tiles, kXcds));
-    if (MODE == kTN) {
-        // (every XCD's list is sized for the most tiles one XCD receives)
-        const int64_t queues = static_cast<int64_t>(g.E) * p.parts, whole = p.tiles / queues;
-        n = kXcds * (whole_queues(queues) ? ceil_div(queues, kXcds) * whole : g.E * ceil_div(whole * p.parts, kXcds));
-    }
+    int64_t n = workgroups(a.g, MODE, p);
     // the largest tiles leave room for one workgroup per CU: that many walk
     // all tiles
     if (p.v == kTile256) n = std::min<int64_t>(n, align_up(compute_units(a.s), kXcds));
@@ -819,6 +879,52 @@ hipError_t start(const Args& a, const Plan& p, void* out) {
     return hipGetLastError();
 }
 
+// Whether both gradients go into one launch.  Not with the largest tiles nor the
+// split kernel's 64 x 64 ones, which leave no room for a second workgroup in a
+// CU's LDS, and not float32's 64 x 64 tiles with 128 x 128: of the former 4
+// workgroups fit a CU, of the pair 2 (16 queues of 256 rows, 512 x 1024: 113 us
+// together, 101 us one after the other).  Otherwise, together and one after the
+// other: bf16, 8 queues of 250 rows, 1000 x 520, 14.8 and 22.9 us; 17 of 289,
+// 648 x 304, 17.9 and 28.0 us; 8 of 1070, 552 x 1608, 65.7 and 66.6 us; one of 2
+// rows, 72 x 248, 5.2 and 8.7 us.
+bool pairs(const moe_grouped_t& g, const Plan& pa, const Plan& pw) {
+    return pa.v != kTile256 && pa.v != kSplit64 && pw.v != kTile256 && !(pa.v == kTile64 && pw.v == kTile128) &&
+           workgroups(g, kNN, pa) + workgroups(g, kTN, pw) < (1 << 24);
+}
+
+template <int TY, int DMB, int DNB, int DNS, int WMB, typename DO, typename WO>
+void start_gradients_of(const moe_grouped_t& g, const Plan& pa, const Plan& pw, const void* dc, const void* w,
+                        const void* a, const int32_t* offsets, void* da, void* dw, hipStream_t s) {
+    const int64_t na = workgroups(g, kNN, pa), nw = workgroups(g, kTN, pw);
+    grouped_gradients_kernel<TY, DMB, DNB, DNS, WMB, DO, WO><<<static_cast<unsigned>(na + nw), 256, 0, s>>>(
+        dc, w, a, offsets, g.E, static_cast<int>(g.rows), g.N, g.K, static_cast<DO*>(da), static_cast<WO*>(dw),
+        static_cast<int>(na), pw.parts);
+}
+
+template <int TY, typename DO, typename WO>
+void start_gradients(const moe_grouped_t& g, const Plan& pa, const Plan& pw, const void* dc, const void* w,
+                     const void* a, const int32_t* offsets, void* da, void* dw, hipStream_t s) {
+    auto go = [&](auto wmb) {
+        constexpr int WMB = decltype(wmb)::value;
+        if (pa.v == kSplit32) {
+            start_gradients_of<TY, 0, 0, 2, WMB, DO, WO>(g, pa, pw, dc, w, a, offsets, da, dw, s);
+        } else if constexpr (TY == kF32) {
+            if constexpr (WMB == 1) start_gradients_of<TY, 1, 1, 2, 1, DO, WO>(g, pa, pw, dc, w, a, offsets, da, dw, s);
+        } else if (pa.v == kTile64x128) {
+            start_gradients_of<TY, 1, 2, 3, WMB, DO, WO>(g, pa, pw, dc, w, a, offsets, da, dw, s);
+        } else {
+            start_gradients_of<TY, 2, 2, 2, WMB, DO, WO>(g, pa, pw, dc, w, a, offsets, da, dw, s);
+        }
+    };
+    if constexpr (TY == kF32) {
+        if (pw.v == kTile64) {
+            go(std::integral_constant<int, 1>{});
+            return;
+        }
+    }
+    go(std::integral_constant<int, 2>{});
+}
+
 }  // namespace
 
 // (of the smallest tile each mode has; parts of queues are made only below 16
@@ -840,26 +946,36 @@ hipError_t launch_grouped_matmul(const moe_grouped_t& g, const void* a, const vo
     return g.dtype == MOE_DTYPE_BF16 ? start<kBf16, kNT, bf16_t>(args, p, c) : start<kF32, kNT, float>(args, p, c);
 }
 
-hipError_t launch_grouped_da(const moe_grouped_t& g, const void* dc, const void* w, const int32_t* offsets, void* da,
-                             hipStream_t s) {
-    const Args args{g, dc, w, offsets, nullptr, nullptr, s};
-    const Plan p = plan_for(g, kNN, false);
-    return g.dtype == MOE_DTYPE_BF16 ? start<kBf16, kNN, bf16_t>(args, p, da) : start<kF32, kNN, float>(args, p, da);
-}
-
-hipError_t launch_grouped_dw(const moe_grouped_t& g, const void* dc, const void* a, const int32_t* offsets, void* dw,
-                             void* ws, hipStream_t s) {
-    const Args args{g, dc, a, offsets, nullptr, nullptr, s};
-    const Plan p = plan_for(g, kTN, false);
+hipError_t launch_grouped_gradients(const moe_grouped_t& g, const void* a, const void* w, const int32_t* offsets,
+                                    const void* dc, void* da, void* dw, void* ws, hipStream_t s) {
     const bool bf16 = g.dtype == MOE_DTYPE_BF16;
-    if (p.parts == 1) return bf16 ? start<kBf16, kTN, bf16_t>(args, p, dw) : start<kF32, kTN, float>(args, p, dw);
-    const hipError_t e = bf16 ? start<kBf16, kTN, float>(args, p, ws) : start<kF32, kTN, float>(args, p, ws);
-    if (e != hipSuccess) return e;
+    if (g.rows == 0) da = nullptr;
+    const Plan pa = plan_for(g, kNN, false), pw = plan_for(g, kTN, false);
+    void* const sums = pw.parts > 1 ? ws : dw;  // float32 if in parts
+    hipError_t e = hipSuccess;
+    if (da != nullptr && dw != nullptr && pairs(g, pa, pw)) {
+        if (!bf16) start_gradients<kF32, float, float>(g, pa, pw, dc, w, a, offsets, da, sums, s);
+        else if (pw.parts > 1) start_gradients<kBf16, bf16_t, float>(g, pa, pw, dc, w, a, offsets, da, sums, s);
+        else start_gradients<kBf16, bf16_t, bf16_t>(g, pa, pw, dc, w, a, offsets, da, sums, s);
+        e = hipGetLastError();
+    } else {
+        if (da != nullptr) {
+            const Args args{g, dc, w, offsets, nullptr, nullptr, s};
+            e = bf16 ? start<kBf16, kNN, bf16_t>(args, pa, da) : start<kF32, kNN, float>(args, pa, da);
+        }
+        if (e == hipSuccess && dw != nullptr) {
+            const Args args{g, dc, a, offsets, nullptr, nullptr, s};
+            if (!bf16) e = start<kF32, kTN, float>(args, pw, sums);
+            else if (pw.parts > 1) e = start<kBf16, kTN, float>(args, pw, sums);
+            else e = start<kBf16, kTN, bf16_t>(args, pw, sums);
+        }
+    }
+    if (e != hipSuccess || dw == nullptr || pw.parts == 1) return e;
     const int64_t n = static_cast<int64_t>(g.E) * g.N * g.K;  // (a multiple of 16)
     const unsigned grid = static_cast<unsigned>(ceil_div(n, 1024));
-    const float* const sums = static_cast<const float*>(ws);
-    if (bf16) grouped_parts_kernel<<<grid, 256, 0, s>>>(sums, n, p.parts, static_cast<bf16_t*>(dw));
-    else grouped_parts_kernel<<<grid, 256, 0, s>>>(sums, n, p.parts, static_cast<float*>(dw));
+    const float* const src = static_cast<const float*>(ws);
+    if (bf16) grouped_parts_kernel<<<grid, 256, 0, s>>>(src, n, pw.parts, static_cast<bf16_t*>(dw));
+    else grouped_parts_kernel<<<grid, 256, 0, s>>>(src, n, pw.parts, static_cast<float*>(dw));
     return hipGetLastError();
 }
 

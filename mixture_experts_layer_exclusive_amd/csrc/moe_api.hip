@@ -654,10 +654,8 @@ moe_status_t moe_grouped_matmul_backward(const moe_grouped_t* g, const void* a, 
         if (dw != nullptr) MOE_TRY(need(a));
     }
     MOE_TRY(need_grouped_ws(*g, MOE_GROUPED_OP_BACKWARD, ws, ws_bytes));
-    hipStream_t s = static_cast<hipStream_t>(stream);
     clear_hip_error();
-    if (da != nullptr && g->rows > 0) MOE_LAUNCH(launch_grouped_da(*g, dc, w, offsets, da, s));
-    if (dw != nullptr) MOE_LAUNCH(launch_grouped_dw(*g, dc, a, offsets, dw, ws, s));
+    MOE_LAUNCH(launch_grouped_gradients(*g, a, w, offsets, dc, da, dw, ws, static_cast<hipStream_t>(stream)));
     return MOE_OK;
 }
 

@@ -166,10 +166,9 @@ size_t grouped_ws_bytes(const moe_grouped_t& g, int op);
 
 hipError_t launch_grouped_matmul(const moe_grouped_t& g, const void* a, const void* w, const int32_t* offsets, void* c,
                                  hipStream_t s);
-hipError_t launch_grouped_da(const moe_grouped_t& g, const void* dc, const void* w, const int32_t* offsets, void* da,
-                             hipStream_t s);
-hipError_t launch_grouped_dw(const moe_grouped_t& g, const void* dc, const void* a, const int32_t* offsets, void* dw,
-                             void* ws, hipStream_t s);
+// (da or dw may be NULL; with rows = 0 only dw is written)
+hipError_t launch_grouped_gradients(const moe_grouped_t& g, const void* a, const void* w, const int32_t* offsets,
+                                    const void* dc, void* da, void* dw, void* ws, hipStream_t s);
 hipError_t launch_grouped_int8(const moe_grouped_t& g, const void* a, const float* a_scales, const void* w,
                                const float* w_scales, const int32_t* offsets, void* c, hipStream_t s);
 hipError_t launch_quant_rows_int8(const void* src, int64_t rows, int cols, int dtype, void* codes, float* scales,
