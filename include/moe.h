@@ -8,6 +8,9 @@
  * SwiGLU feed-forward over its queue; a gate-weighted combine returns the
  * results to token order.
  *
+ * Beside it: the products by expert one at a time, with their gradients and
+ * in 8-bit integers, for experts of another form (moe_grouped_*).
+ *
  * Sources (summaries of three papers; they give the structure, not the
  * formulas):
  *   - MoEBlaze summary (euno.news, "MoEBlaze: breaking the memory wall for

@@ -1,7 +1,8 @@
 """One GPU's MoE-layer forward on MI355X (gfx950): router GEMM and static
 top-k gating, counting-sort dispatch queues, grouped SwiGLU expert FFN on
-bf16 MFMA, gate-weighted combine; and the layer's backward on the same
-queues.
+bf16 MFMA, gate-weighted combine; the layer's backward on the same queues;
+and the products by expert on their own, with their gradients and in 8-bit
+integers.
 
 The kernels live in ``libmoe.so`` (C ABI in ``include/moe.h``); this package
 only binds them to torch tensors and streams.
