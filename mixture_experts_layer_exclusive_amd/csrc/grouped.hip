@@ -60,7 +60,9 @@ struct TileLds {
     static constexpr int EPI_AT = STREAM ? NS * STAGE : 0;
     static constexpr int Q_AT = NS * STAGE + (STREAM ? 4 * EPI : 0);
     static_assert(4 * EPI <= NS * STAGE, "the staged outputs must fit the stages");
-    static constexpr int BYTES = Q_AT + sizeof(Queues) + 512;
+    static constexpr int RING_AT = Q_AT + sizeof(Queues);
+    static constexpr int DEAL_AT = RING_AT + 512;
+    static constexpr int BYTES = DEAL_AT + (STREAM ? sizeof(Deal) : 0);
     static_assert(BYTES <= 160 * 1024, "LDS");
 };
 
@@ -104,9 +106,42 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
     load_queues<MODE == kTN>(offsets, E, rows, TM, queues);
     const int xcd = block % kXcds;
     const int stride = blocks / kXcds;
+    // weight gradients: how their tiles are dealt.  A stream's queues are uneven
+    // if the longest is over 1.25 times the mean.  Few of them (below 32) then
+    // go over all XCDs (8 queues of 4096 rows in the mean, 4096 x 2048: 442 us, one
+    // queue to each XCD 557 us); more are dealt by load where the work is worth
+    // it: from half a slice per workgroup and expert (128 queues, 768 x 2048, of
+    // 512 rows, 96 slices: 259 us, in snake order 275; of 256 rows, 48 slices: 155
+    // and 148).
+    bool dealt = MODE == kTN && whole_queues(static_cast<int64_t>(E) * parts), uneven = false;
+    Deal& deal = *reinterpret_cast<Deal*>(smem + (STREAM ? Lds::DEAL_AT : 0));
+    const int tiles_of_queue = ((N + TM - 1) / TM) * ((K + TN - 1) / TN);
+    if constexpr (MODE == kTN && STREAM) {
+        const int e = queues.order[0];
+        const int64_t longest = __builtin_amdgcn_readfirstlane(queues.hi[e] - queues.lo[e]);
+        if (parts == 1 && dealt && stride <= 32 && longest * 4 * E > static_cast<int64_t>(rows) * 5) {
+            uneven = E >= 32 && 2 * static_cast<int64_t>(rows) * tiles_of_queue >= static_cast<int64_t>(E) * QS * blocks;
+            dealt = E >= 32;
+            if (uneven) deal_queues(queues, E, QS, tiles_of_queue, xcd, block / kXcds, stride, deal);
+        }
+    }
+    int dealt_queue = 0, dealt_tile = 0;         // uneven: the next tile
     auto tile_at = [&](int place, Tile& t) -> Found {
         if constexpr (MODE == kTN) {
-            return weight_tile(queues, E, N, K, TM, TN, QS, parts, xcd, place, t);
+            if (STREAM && uneven) {
+                const int full = quick_div(tiles_of_queue, stride), rest = tiles_of_queue - full * stride;
+                for (; dealt_queue < __builtin_amdgcn_readfirstlane(deal.queues); ++dealt_queue, dealt_tile = 0) {
+                    const int last = __builtin_amdgcn_readfirstlane(static_cast<int>(deal.place[dealt_queue]));
+                    if (dealt_tile >= full + (last < rest ? 1 : 0)) continue;
+                    const int local = dealt_tile * stride + (dealt_tile < full ? block / kXcds : last);
+                    ++dealt_tile;
+                    weight_tile_of(queues, __builtin_amdgcn_readfirstlane(static_cast<int>(deal.expert[dealt_queue])), 0,
+                                   local, E, N, K, TM, TN, QS, 1, t);
+                    return kTile;
+                }
+                return kEnd;
+            }
+            return weight_tile(queues, E, N, K, TM, TN, QS, parts, dealt, xcd, place, t);
         } else {
             t.q0 = 0;
             t.q1 = MODE == kNT ? K : N;
@@ -168,7 +203,7 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
     };
     // the tiles between the load side and the multiplying side (at most two, of
     // one slice each, and the one being multiplied), kept by each wave for itself
-    int* const ring = reinterpret_cast<int*>(smem + Q_AT + sizeof(Queues)) + wave * 32;
+    int* const ring = reinterpret_cast<int*>(smem + Lds::RING_AT) + wave * 32;
     int loading = 0;                             // tiles the load side has begun
     // the next tile; after the last, every load is out of range
     auto next_load = [&]() {
@@ -495,7 +530,8 @@ __device__ __forceinline__ void grouped_split(char* __restrict__ smem, int block
     {
         const int xcd = block % kXcds, place = block / kXcds;
         if constexpr (MODE == kTN) {
-            if (weight_tile(queues, E, N, K, TM, TN, QS, parts, xcd, place, t) != kTile) return;
+            if (weight_tile(queues, E, N, K, TM, TN, QS, parts, whole_queues(static_cast<int64_t>(E) * parts), xcd, place, t) != kTile)
+                return;
         } else {
             t.q0 = 0;
             t.q1 = MODE == kNT ? K : N;

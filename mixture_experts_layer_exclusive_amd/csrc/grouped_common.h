@@ -148,41 +148,11 @@ __device__ __forceinline__ Found row_tile(const Queues& q, int E, int bm, int bn
     return t.m0 >= lo && t.m0 < t.m1 ? kTile : kSkip;
 }
 
-// kTN.  With parts > 1 each queue is cut into that many ranges of rows
-// (multiples of qs), each with tiles of its own whose sums go to matrix part *
-// E + e.  A tile's cost is its queue's length, so the experts are dealt longest
-// first.  Each XCD takes whole (parts of) queues, in a snake order, XCD 0 to 7
-// and back: their tiles read the same two operand blocks and share its L2
-// (dealing every expert's tiles over all XCDs: 128 queues of 2048 rows, 768 x
-// 2048, 970 us against 870).  With too few of them to keep the XCDs even, every
-// XCD takes an eighth of each expert's tiles instead.  Within a queue, groups of
-// kGroupM row tiles walk the column tiles.
-__host__ __device__ __forceinline__ bool whole_queues(int64_t queues) { return queues >= 32 || queues % kXcds == 0; }
-
-__device__ __forceinline__ Found weight_tile(const Queues& q, int E, int M, int P, int bm, int bn, int qs, int parts,
-                                             int xcd, int place, Tile& t) {
+// kTN: tile `local` of (part `part` of) expert e's weight gradient.  Within it,
+// groups of kGroupM row tiles walk the column tiles.
+__device__ __forceinline__ void weight_tile_of(const Queues& q, int e, int part, int local, int E, int M, int P, int bm,
+                                               int bn, int qs, int parts, Tile& t) {
     const int mtn = (M + bm - 1) / bm, ptn = (P + bn - 1) / bn;
-    const int whole = mtn * ptn;
-    int rank, part, local;
-    if (whole_queues(E * parts)) {
-        const int j = quick_div(place, whole);
-        if (j * kXcds >= E * parts) return kEnd;
-        const int i = j * kXcds + (j & 1 ? kXcds - 1 - xcd : xcd);
-        if (i >= E * parts) return kSkip;
-        rank = quick_div(i, parts);
-        part = i - rank * parts;
-        local = place - j * whole;
-    } else {
-        const int per_e = whole * parts;
-        const int per_x = (per_e + kXcds - 1) / kXcds;
-        rank = quick_div(place, per_x);
-        if (rank >= E) return kEnd;
-        local = ((xcd + rank) & (kXcds - 1)) * per_x + place - rank * per_x;
-        if (local >= per_e) return kSkip;
-        part = quick_div(local, whole);
-        local -= part * whole;
-    }
-    const int e = __builtin_amdgcn_readfirstlane(static_cast<int>(q.order[rank]));
     const int group = quick_div(local, kGroupM * ptn);
     const int first = group * kGroupM;
     const int gsz = min(kGroupM, mtn - first);
@@ -200,7 +170,100 @@ __device__ __forceinline__ Found weight_tile(const Queues& q, int E, int M, int 
         t.q0 = min(t.q0 + part * per, t.q1);
         t.q1 = min(t.q0 + per, t.q1);
     }
+}
+
+// kTN.  With parts > 1 each queue is cut into that many ranges of rows
+// (multiples of qs), each with tiles of its own whose sums go to matrix part *
+// E + e.  A tile's cost is its queue's length, so the experts are dealt longest
+// first.  Each XCD takes whole (parts of) queues, in a snake order, XCD 0 to 7
+// and back: their tiles read the same two operand blocks and share its L2
+// (dealing every expert's tiles over all XCDs: 128 queues of 2048 rows, 768 x
+// 2048, 970 us against 870).  With too few of them to keep the XCDs even, every
+// XCD takes an eighth of each expert's tiles instead.
+__host__ __device__ __forceinline__ bool whole_queues(int64_t queues) { return queues >= 32 || queues % kXcds == 0; }
+
+__device__ __forceinline__ Found weight_tile(const Queues& q, int E, int M, int P, int bm, int bn, int qs, int parts,
+                                             bool dealt, int xcd, int place, Tile& t) {
+    const int whole = ((M + bm - 1) / bm) * ((P + bn - 1) / bn);
+    int rank, part, local;
+    if (dealt) {
+        const int j = quick_div(place, whole);
+        if (j * kXcds >= E * parts) return kEnd;
+        const int i = j * kXcds + (j & 1 ? kXcds - 1 - xcd : xcd);
+        if (i >= E * parts) return kSkip;
+        rank = quick_div(i, parts);
+        part = i - rank * parts;
+        local = place - j * whole;
+    } else {
+        const int per_e = whole * parts;
+        const int per_x = (per_e + kXcds - 1) / kXcds;
+        rank = quick_div(place, per_x);
+        if (rank >= E) return kEnd;
+        local = ((xcd + rank) & (kXcds - 1)) * per_x + place - rank * per_x;
+        if (local >= per_e) return kSkip;
+        part = quick_div(local, whole);
+        local -= part * whole;
+    }
+    weight_tile_of(q, __builtin_amdgcn_readfirstlane(static_cast<int>(q.order[rank])), part, local, E, M, P, bm, bn, qs,
+                   parts, t);
     return kTile;
+}
+
+// kTN, many uneven queues and workgroups that each walk several tiles: the
+// experts, longest first, each to the XCD that has the least so far; and of
+// an expert's `whole` tiles, one more to those of the XCD's `stride` (at most
+// 32) workgroups that have the least.  128 queues of 2048 rows in the mean, the
+// longest of 19000, 768 x 2048: 753 us, 822 us in the snake order; 64 queues,
+// 1408 x 2048: 1293 and 1436 us.  Filled by the first wave, the same in every
+// workgroup, in 0.05 to 0.1 us per expert; costs are counted in slices, a tile's
+// start as two.  (Sums that overflow would only deal badly: the places stay a
+// permutation.)
+struct Deal {
+    int queues;                                // of this XCD
+    unsigned char expert[MOE_MAX_EXPERTS];
+    unsigned char place[MOE_MAX_EXPERTS];      // this workgroup's place for the queue's last, partial round
+};
+
+__device__ __forceinline__ uint32_t min_of_8(uint32_t v) {
+    // within each 8 lanes: neighbours, pairs, fours
+    v = min(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0xB1, 0xf, 0xf, true)));
+    v = min(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x4E, 0xf, 0xf, true)));
+    return min(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x141, 0xf, 0xf, true)));
+}
+
+__device__ __forceinline__ void deal_queues(const Queues& q, int E, int qs, int whole, int xcd, int at, int stride,
+                                            Deal& d) {
+    if (threadIdx.x < 64) {
+        const uint32_t lane = threadIdx.x;
+        const int full = whole / stride, rest = whole - full * stride;
+        uint32_t on_xcd = 0, on_cu = 0;        // lane i: what XCD i, and workgroup i of this XCD, have so far
+        int n = 0;
+        for (int i0 = 0; i0 < E; i0 += 64) {
+            const int e = i0 + static_cast<int>(lane) < E ? q.order[i0 + lane] : 0;
+            const int cost = max((q.hi[e] - q.lo[e] + qs - 1) / qs, 1) + 2;
+            for (int i = 0; i < min(64, E - i0); ++i) {
+                const uint32_t c = __builtin_amdgcn_readlane(cost, i);
+                const uint32_t to = __builtin_amdgcn_readfirstlane(min_of_8((on_xcd << 3) | (lane & 7))) & 7;
+                on_xcd += (lane & 7) == to ? c : 0;
+                if (static_cast<int>(to) != xcd) continue;
+                const uint32_t key = static_cast<int>(lane) < stride ? (on_cu << 6) | lane : ~0u;
+                int rank = 0;
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    rank += static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(key), j)) < key ? 1 : 0;
+                on_cu += c * (full + (rank < rest ? 1 : 0));
+                const int mine = __builtin_amdgcn_readlane(rank, at);
+                const int expert = __builtin_amdgcn_readlane(e, i);
+                if (lane == 0) {
+                    d.expert[n] = static_cast<unsigned char>(expert);
+                    d.place[n] = static_cast<unsigned char>(mine);
+                }
+                ++n;
+            }
+        }
+        if (lane == 0) d.queues = n;
+    }
+    __syncthreads();
 }
 
 // ---- global -> LDS -----------------------------------------------------------

@@ -237,6 +237,8 @@ CHOICES = [
     ("backward", "bf16", 21678, 3, 1488, 144),
     ("backward", "bf16", 35168, 5, 528, 336),
     ("backward", "bf16", 3061, 16, 3600, 464),
+    ("backward", "bf16", 56000, 40, 304, 520),
+    ("backward", "bf16", 9000, 34, 1272, 2040),
     ("backward", "f32", 3061, 16, 3600, 464),
     ("backward", "f32", 13, 1, 3536, 4144),
     ("backward", "f32", 15230, 3, 128, 1536),
