@@ -109,19 +109,20 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
     // weight gradients: how their tiles are dealt.  A stream's queues are uneven
     // if the longest is over 1.25 times the mean.  Few of them (below 32) then
     // go over all XCDs (8 queues of 4096 rows in the mean, 4096 x 2048: 442 us, one
-    // queue to each XCD 557 us); more are dealt by load where the work is worth
-    // it: from half a slice per workgroup and expert (128 queues, 768 x 2048, of
-    // 512 rows, 96 slices: 259 us, in snake order 275; of 256 rows, 48 slices: 155
-    // and 148).
+    // queue to each XCD 557 us; with smaller tiles, whose problems are small, it
+    // changes nothing); more are dealt by load where the work is worth it: from
+    // half a slice per workgroup and expert (128 queues, 768 x 2048, of 512 rows,
+    // 96 slices: 259 us, in snake order 275; of 256 rows, 48 slices: 155 and 148).
     bool dealt = MODE == kTN && whole_queues(static_cast<int64_t>(E) * parts), uneven = false;
     Deal& deal = *reinterpret_cast<Deal*>(smem + (STREAM ? Lds::DEAL_AT : 0));
     const int tiles_of_queue = ((N + TM - 1) / TM) * ((K + TN - 1) / TN);
     if constexpr (MODE == kTN && STREAM) {
         const int e = queues.order[0];
         const int64_t longest = __builtin_amdgcn_readfirstlane(queues.hi[e] - queues.lo[e]);
-        if (parts == 1 && dealt && stride <= 32 && longest * 4 * E > static_cast<int64_t>(rows) * 5) {
-            uneven = E >= 32 && 2 * static_cast<int64_t>(rows) * tiles_of_queue >= static_cast<int64_t>(E) * QS * blocks;
+        if (parts == 1 && dealt && longest * 4 * E > static_cast<int64_t>(rows) * 5) {
             dealt = E >= 32;
+            uneven = dealt && stride <= 32 &&
+                     2 * static_cast<int64_t>(rows) * tiles_of_queue >= static_cast<int64_t>(E) * QS * blocks;
             if (uneven) deal_queues(queues, E, QS, tiles_of_queue, xcd, block / kXcds, stride, deal);
         }
     }
@@ -506,11 +507,11 @@ template <int TY, int MODE, int MB, int NB, typename O>
 __device__ __forceinline__ void grouped_split(char* __restrict__ smem, int block, const void* __restrict__ Xp,
                                               const void* __restrict__ Yp, const int32_t* __restrict__ offsets, int E,
                                               int rows, int N, int K, O* __restrict__ C, const float* __restrict__ sx,
-                                              const float* __restrict__ sy, int parts) {
-    constexpr bool XC = MODE == kTN, YC = MODE != kNT;
-    static_assert(TY != kI8 || MODE == kNT, "int8: forward only");
+                                              const float* __restrict__ sy) {
+    static_assert(MODE != kTN && (TY != kI8 || MODE == kNT), "no weight gradients; int8: forward only");
+    constexpr bool YC = MODE != kNT;
     constexpr int TM = 32 * MB, TN = 32 * NB;
-    using XS = Slice<TY, XC, TM>;
+    using XS = Slice<TY, false, TM>;
     using YS = Slice<TY, YC, TN>;
     constexpr int EB = XS::EB;
     constexpr int QS = 128 / EB;
@@ -526,18 +527,10 @@ __device__ __forceinline__ void grouped_split(char* __restrict__ smem, int block
 
     const int P = MODE == kNT ? N : K;
     Tile t;
-    load_queues<MODE == kTN>(offsets, E, rows, TM, queues);
-    {
-        const int xcd = block % kXcds, place = block / kXcds;
-        if constexpr (MODE == kTN) {
-            if (weight_tile(queues, E, N, K, TM, TN, QS, parts, whole_queues(static_cast<int64_t>(E) * parts), xcd, place, t) != kTile)
-                return;
-        } else {
-            t.q0 = 0;
-            t.q1 = MODE == kNT ? K : N;
-            if (row_tile(queues, E, TM, TN, P, xcd, place, t) != kTile) return;
-        }
-    }
+    load_queues<false>(offsets, E, rows, TM, queues);
+    t.q0 = 0;
+    t.q1 = MODE == kNT ? K : N;
+    if (row_tile(queues, E, TM, TN, P, block % kXcds, block / kXcds, t) != kTile) return;
     __syncthreads();  // every lookup is done before the loads overwrite the table
 
     const int tid = threadIdx.x;
@@ -545,17 +538,14 @@ __device__ __forceinline__ void grouped_split(char* __restrict__ smem, int block
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t xrow = static_cast<int64_t>(MODE == kNT ? K : N) * EB;
     const int64_t yrow = static_cast<int64_t>(K) * EB;
-    const int64_t xstep = XC ? QS * xrow : 128, ystep = YC ? QS * yrow : 128;
+    const int64_t xstep = 128, ystep = YC ? QS * yrow : 128;
     const int nk = (t.q1 - t.q0 + QS - 1) / QS;
     const int qtail = t.q1 - t.q0 - (nk - 1) * QS;
-    const uint64_t xbase = uniform64(
-        reinterpret_cast<uint64_t>(Xp) +
-        static_cast<uint64_t>(XC ? t.q0 * xrow + static_cast<int64_t>(t.m0) * EB : t.m0 * xrow));
+    const uint64_t xbase = uniform64(reinterpret_cast<uint64_t>(Xp) + static_cast<uint64_t>(t.m0 * xrow));
     const uint64_t ybase = uniform64(
         reinterpret_cast<uint64_t>(Yp) +
-        static_cast<uint64_t>(MODE == kTN   ? t.q0 * yrow + static_cast<int64_t>(t.p0) * EB
-                              : MODE == kNN ? static_cast<int64_t>(t.e) * N * yrow + static_cast<int64_t>(t.p0) * EB
-                                            : (static_cast<int64_t>(t.e) * N + t.p0) * yrow));
+        static_cast<uint64_t>(MODE == kNN ? static_cast<int64_t>(t.e) * N * yrow + static_cast<int64_t>(t.p0) * EB
+                                          : (static_cast<int64_t>(t.e) * N + t.p0) * yrow));
     const uint32_t lds_w = __builtin_amdgcn_readfirstlane(lds_addr(smem)) + wave * RING;
     char* const mine = smem + wave * RING;
     uint32_t xoff[XS::LOADS], yoff[YS::LOADS], xtail = 0, ytail = 0;
@@ -569,7 +559,7 @@ __device__ __forceinline__ void grouped_split(char* __restrict__ smem, int block
         yoff[j] = YS::offset(j, lane, static_cast<uint32_t>(yrow), P - t.p0);
         ytail |= (YS::beyond(j, lane, qtail) ? 1u : 0u) << j;
     }
-    const Fragments<TY, XC, TM, MB> xfrag(lane, 0);
+    const Fragments<TY, false, TM, MB> xfrag(lane, 0);
     const Fragments<TY, YC, TN, NB> yfrag(lane, 0);
     Acc<TY> acc[NB][MB];
 #pragma unroll
@@ -631,7 +621,7 @@ __device__ __forceinline__ void grouped_split(char* __restrict__ smem, int block
         }
         wait_vmcnt<0>();
     };
-    if constexpr (!XC && MB == 1) {
+    if constexpr (MB == 1) {
         const int nx = (t.m1 - t.m0 + 7) / 8;
         if (nx == 1) stream(std::integral_constant<int, 1>{});
         else if (nx == 2) stream(std::integral_constant<int, 2>{});
@@ -673,7 +663,7 @@ __device__ __forceinline__ void grouped_split(char* __restrict__ smem, int block
         } else {
             o = v;
         }
-        O* const dst = C + (MODE == kTN ? static_cast<int64_t>(t.e) * N * K : 0) + static_cast<int64_t>(m) * P + col;
+        O* const dst = C + static_cast<int64_t>(m) * P + col;
         if constexpr (sizeof(O) == 4) *reinterpret_cast<f32x4_t*>(dst) = o;
         else *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
     }
@@ -682,9 +672,9 @@ __device__ __forceinline__ void grouped_split(char* __restrict__ smem, int block
 template <int TY, int MODE, int MB, int NB, typename O>
 __global__ __launch_bounds__(256) void grouped_split_kernel(
     const void* __restrict__ Xp, const void* __restrict__ Yp, const int32_t* __restrict__ offsets, int E, int rows,
-    int N, int K, O* __restrict__ C, const float* __restrict__ sx, const float* __restrict__ sy, int parts) {
+    int N, int K, O* __restrict__ C, const float* __restrict__ sx, const float* __restrict__ sy) {
     __shared__ __attribute__((aligned(1024))) char smem[split_lds(MB, NB)];
-    grouped_split<TY, MODE, MB, NB, O>(smem, blockIdx.x, Xp, Yp, offsets, E, rows, N, K, C, sx, sy, parts);
+    grouped_split<TY, MODE, MB, NB, O>(smem, blockIdx.x, Xp, Yp, offsets, E, rows, N, K, C, sx, sy);
 }
 
 // ---- both gradients in one launch -----------------------------------------------
@@ -704,7 +694,7 @@ __global__ __launch_bounds__(256, 2) void grouped_gradients_kernel(
     const int block = blockIdx.x;
     if (block < da_blocks) {
         if constexpr (DMB == 0)
-            grouped_split<TY, kNN, 1, 1, DO>(smem, block, dc, w, offsets, E, rows, N, K, da, nullptr, nullptr, 1);
+            grouped_split<TY, kNN, 1, 1, DO>(smem, block, dc, w, offsets, E, rows, N, K, da, nullptr, nullptr);
         else
             grouped_tile<TY, kNN, DMB, DNB, DNS, DO>(smem, block, da_blocks, dc, w, offsets, E, rows, N, K, da, nullptr,
                                                      nullptr, 1);
@@ -871,9 +861,9 @@ void start_tile(const Args& a, const Plan& p, unsigned grid, O* C) {
         a.X, a.Y, a.offsets, a.g.E, static_cast<int>(a.g.rows), a.g.N, a.g.K, C, a.sx, a.sy, p.parts);
 }
 template <int TY, int MODE, int MB, int NB, typename O>
-void start_split(const Args& a, const Plan& p, unsigned grid, O* C) {
+void start_split(const Args& a, unsigned grid, O* C) {
     grouped_split_kernel<TY, MODE, MB, NB, O><<<grid, 256, 0, a.s>>>(
-        a.X, a.Y, a.offsets, a.g.E, static_cast<int>(a.g.rows), a.g.N, a.g.K, C, a.sx, a.sy, p.parts);
+        a.X, a.Y, a.offsets, a.g.E, static_cast<int>(a.g.rows), a.g.N, a.g.K, C, a.sx, a.sy);
 }
 
 // Workgroups that plan p takes, one per tile: a multiple of 8.
@@ -901,12 +891,12 @@ hipError_t start(const Args& a, const Plan& p, void* out) {
             start_tile<TY, MODE, 2, 2, 2>(a, p, grid, C);
         }
     } else if constexpr (TY == kF32) {
-        if (p.v == kSplit32) start_split<TY, MODE, 1, 1>(a, p, grid, C);
+        if (p.v == kSplit32) start_split<TY, MODE, 1, 1>(a, grid, C);
         else start_tile<TY, MODE, 1, 1, 2>(a, p, grid, C);
     } else {
         switch (p.v) {
-            case kSplit32: start_split<TY, MODE, 1, 1>(a, p, grid, C); break;
-            case kSplit64: start_split<TY, MODE, 2, 2>(a, p, grid, C); break;
+            case kSplit32: start_split<TY, MODE, 1, 1>(a, grid, C); break;
+            case kSplit64: start_split<TY, MODE, 2, 2>(a, grid, C); break;
             case kTile64x128: start_tile<TY, MODE, 1, 2, 3>(a, p, grid, C); break;
             case kTile256: start_tile<TY, MODE, 4, 4, 2>(a, p, grid, C); break;
             default: start_tile<TY, MODE, 2, 2, 2>(a, p, grid, C); break;
