@@ -114,8 +114,11 @@ __device__ __forceinline__ int quick_div(int a, int b) {
 
 // kNT, kNN.  Workgroups are dealt to the 8 XCDs round-robin; each XCD walks one
 // contiguous range of the tile order, `place` counting within it.  The order
-// groups kGroupM row tiles per column tile, so that the tiles running on one
-// XCD at a time share operand rows in its L2.
+// groups row tiles per column tile, so that the tiles running on one XCD at a
+// time share operand rows in its L2: kGroupM of them, or half as many for tiles
+// of 256 in at most 8 columns, so that the 32 workgroups of an XCD span whole
+// rows of C and read them once (bf16, 128 queues of 2048 rows, 2048 x 768: 798 us, in
+// groups of 8 861; 8 queues, 14336 x 4096, 56 columns: 1493 and 1468 us).
 __device__ __forceinline__ Found row_tile(const Queues& q, int E, int bm, int bn, int P, int xcd, int place,
                                           Tile& t) {
     const int total_m = __builtin_amdgcn_readfirstlane(q.end[E - 1]);
@@ -127,10 +130,11 @@ __device__ __forceinline__ Found row_tile(const Queues& q, int E, int bm, int bn
     const int per_xcd = (total + kXcds - 1) / kXcds;
     const int id = xcd * per_xcd + place;
     if (place >= per_xcd || id >= total) return kEnd;
-    const int group = quick_div(id, kGroupM * ptiles);
-    const int first = group * kGroupM;
-    const int gsz = min(kGroupM, total_m - first);
-    const int local = id - group * kGroupM * ptiles;
+    const int height = bm == 256 && ptiles <= 8 ? kGroupM / 2 : kGroupM;
+    const int group = quick_div(id, height * ptiles);
+    const int first = group * height;
+    const int gsz = min(height, total_m - first);
+    const int local = id - group * height * ptiles;
     const int pt = quick_div(local, gsz);
     const int mt = first + local - pt * gsz;
     // the expert: how many experts' tiles end at or before mt
