@@ -625,6 +625,50 @@ def test_calls_on_two_streams_at_once():
             assert torch.equal(v, ref[key]), key
 
 
+def test_streams_of_tiles_at_once_and_replayed():
+    """The largest tiles' workgroups fill the card and walk many tiles each:
+    two such calls at once on two streams, and both captured and replayed
+    between other work, give the bits of one call alone."""
+    states = [graph_state(ragged(9000, 34, seed=s), 1272, 2048, 80 + s) for s in (1, 2)]
+    refs = []
+    for st in states:
+        all_outputs(*st)
+        torch.cuda.synchronize()
+        refs.append({key: v.clone() for key, v in outputs(st).items()})
+
+    def clear():
+        for st in states:
+            for v in outputs(st).values():
+                v.zero_()
+        torch.cuda.synchronize()
+
+    def compare(what):
+        torch.cuda.synchronize()
+        for st, ref in zip(states, refs):
+            for key, v in outputs(st).items():
+                assert torch.equal(v, ref[key]), (what, key)
+
+    streams = [torch.cuda.Stream() for _ in states]
+    clear()
+    for s, st in zip(streams, states):
+        with torch.cuda.stream(s):
+            all_outputs(*st)
+    compare("two streams")
+    graphs = []
+    for st in states:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            all_outputs(*st)
+        graphs.append(g)
+    for it in range(3):
+        clear()
+        _ = (states[0][0].float() * 2).sum().item()
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        compare(f"replay {it}")
+
+
 def test_more_than_2_31_elements():
     """Row offsets past 2^31 elements of c, a and dc, and past 2^32 bytes of
     w: sampled rows against the oracle."""
