@@ -595,7 +595,10 @@ __device__ __forceinline__ void grouped_split(char* __restrict__ smem, int block
         };
         dma(wave, 0);
         dma(wave + 4, STAGE);
+        // (the compiler does not know what the loads write: it keeps LDS accesses
+        // behind each wait because of the empty statement)
         wait_vmcnt<NL>();
+        asm volatile("" ::: "memory");
         read(0, 0);
         wait_vmcnt_lgkm0<63>();
         __builtin_amdgcn_sched_barrier(0);
@@ -620,6 +623,7 @@ __device__ __forceinline__ void grouped_split(char* __restrict__ smem, int block
             }
         }
         wait_vmcnt<0>();
+        asm volatile("" ::: "memory");
     };
     if constexpr (MB == 1) {
         const int nx = (t.m1 - t.m0 + 7) / 8;
