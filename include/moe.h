@@ -383,7 +383,9 @@ moe_status_t moe_expert_ffn_fp8(const moe_problem_t* p, const void* x, const int
  * fewer than 2^24 - 2^11 output tiles (rows * max(N, K, 32) and E * N * K up
  * to 2^32 always fit).  Outputs must not overlap the inputs.
  * Workspace: moe_grouped_workspace_size of the same problem; ws may be NULL
- * when that is 0.  No atomics: the same inputs give the same bits.
+ * when that is 0.  Only a weight gradient ever needs one: for the forward and
+ * the 8-bit integer product the size is 0, and their ws and ws_bytes are not
+ * looked at.  No atomics: the same inputs give the same bits.
  */
 #define MOE_GROUPED_MAX_DIM (1 << 20)
 
@@ -406,7 +408,8 @@ moe_status_t moe_grouped_matmul(const moe_grouped_t* g, const void* a, const voi
  *   da[r, k] = sum_n dc[r, n] * w[e, n, k]        (rows r of expert e's queue)
  *   dw[e, n, k] = sum over the queue's rows r of dc[r, n] * a[r, k]
  * Either of da [rows, K] and dw [E, N, K] may be NULL (then it is not
- * computed, and w, respectively a, may be NULL too), not both.  An empty
+ * computed, and w, respectively a, may be NULL too), not both.  Without dw
+ * no workspace is needed, whatever its size for the problem.  An empty
  * queue gives dw[e] = 0; with rows = 0 only dw is written, and a and dc may
  * be NULL.  Accumulation and rounding as in the forward.
  */

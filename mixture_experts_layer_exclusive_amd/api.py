@@ -511,11 +511,12 @@ def grouped_workspace_size(op: int, rows: int, E: int, N: int, K: int, dtype) ->
     return _grouped_plan(op, rows, E, N, K, dtype)[1]
 
 
-def _grouped(op: int, rows: int, E: int, N: int, K: int, dtype, device, ws: Optional[torch.Tensor]):
+def _grouped(op: int, rows: int, E: int, N: int, K: int, dtype, device, ws: Optional[torch.Tensor],
+             uses_ws: bool = True):
     """(problem struct, workspace, its bytes) of a grouped product's call."""
     g, need = _grouped_plan(op, rows, E, N, K, dtype)
     if ws is None:
-        if need == 0:
+        if need == 0 or not uses_ws:
             return g, None, 0
         ws = torch.empty(need, dtype=torch.uint8, device=device)
     else:
@@ -553,8 +554,9 @@ def grouped_matmul_backward(a: Optional[torch.Tensor], w: Optional[torch.Tensor]
                             ws: Optional[torch.Tensor] = None, out: Optional[dict] = None) -> dict:
     """Gradients of ``grouped_matmul`` for dc [R, N]: da [R, K] (rows that no
     queue holds are not written) and dw [E, N, K] (zero for an empty queue),
-    each None when not asked for.  Without ``with_dw`` a may be None, without
-    ``with_da`` w.  ``out`` may supply either tensor."""
+    each None when not asked for.  Without ``with_dw`` a may be None and no
+    workspace is needed, without ``with_da`` w may be None.  ``out`` may
+    supply either tensor."""
     if not (with_da or with_dw):
         raise ValueError("with_da or with_dw is required")
     if dc.dim() != 2 or (a is not None and a.dim() != 2) or (w is not None and w.dim() != 3):
@@ -573,7 +575,8 @@ def grouped_matmul_backward(a: Optional[torch.Tensor], w: Optional[torch.Tensor]
     res = dict(out or {})
     _expect("da", res.get("da"), (R, K), dt, dev, required=False)
     _expect("dw", res.get("dw"), (E, N, K), dt, dev, required=False)
-    g, ws, nbytes = _grouped(L.MOE_GROUPED_OP_BACKWARD, R, E, N, K, dt, dev, ws)
+    # (the workspace holds partial sums of dw)
+    g, ws, nbytes = _grouped(L.MOE_GROUPED_OP_BACKWARD, R, E, N, K, dt, dev, ws, uses_ws=with_dw)
     if not with_da:
         res["da"] = None
     elif res.get("da") is None:

@@ -184,9 +184,9 @@ moe_status_t check_grouped(const moe_grouped_t* g, bool int8) {
     return MOE_OK;
 }
 
-// The workspace of a grouped product: required only when it needs one.
-moe_status_t need_grouped_ws(const moe_grouped_t& g, int op, const void* ws, size_t ws_bytes) {
-    const size_t bytes = grouped_ws_bytes(g, op);
+// The workspace of a weight gradient: required only when it needs one.
+moe_status_t need_grouped_ws(const moe_grouped_t& g, const void* ws, size_t ws_bytes) {
+    const size_t bytes = grouped_ws_bytes(g, MOE_GROUPED_OP_BACKWARD);
     if (bytes == 0) return MOE_OK;
     MOE_TRY(need(ws));
     return ws_bytes < bytes ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
@@ -627,14 +627,13 @@ moe_status_t moe_grouped_workspace_size(const moe_grouped_t* g, int32_t op, size
 }
 
 moe_status_t moe_grouped_matmul(const moe_grouped_t* g, const void* a, const void* w, const int32_t* offsets,
-                                void* c, void* ws, size_t ws_bytes, void* stream) {
+                                void* c, void*, size_t, void* stream) {
     MOE_TRY(check_grouped(g, false));
     if (g->rows == 0) return MOE_OK;
     MOE_TRY(need(a));
     MOE_TRY(need(w));
     MOE_TRY(need(offsets));
     MOE_TRY(need(c));
-    MOE_TRY(need_grouped_ws(*g, MOE_GROUPED_OP_MATMUL, ws, ws_bytes));
     clear_hip_error();
     MOE_LAUNCH(launch_grouped_matmul(*g, a, w, offsets, c, static_cast<hipStream_t>(stream)));
     return MOE_OK;
@@ -653,7 +652,7 @@ moe_status_t moe_grouped_matmul_backward(const moe_grouped_t* g, const void* a, 
         if (da != nullptr) MOE_TRY(need(w));
         if (dw != nullptr) MOE_TRY(need(a));
     }
-    MOE_TRY(need_grouped_ws(*g, MOE_GROUPED_OP_BACKWARD, ws, ws_bytes));
+    if (dw != nullptr) MOE_TRY(need_grouped_ws(*g, ws, ws_bytes));
     clear_hip_error();
     MOE_LAUNCH(launch_grouped_gradients(*g, a, w, offsets, dc, da, dw, ws, static_cast<hipStream_t>(stream)));
     return MOE_OK;
@@ -675,8 +674,8 @@ moe_status_t moe_quantize_rows_int8(const void* src, int64_t rows, int32_t cols,
 }
 
 moe_status_t moe_grouped_matmul_int8(const moe_grouped_t* g, const void* a, const float* a_scales, const void* w,
-                                     const float* w_scales, const int32_t* offsets, void* c, void* ws,
-                                     size_t ws_bytes, void* stream) {
+                                     const float* w_scales, const int32_t* offsets, void* c, void*, size_t,
+                                     void* stream) {
     MOE_TRY(check_grouped(g, true));
     if (offsets == nullptr && g->E != 1) return MOE_ERR_INVALID_ARGUMENT;
     if (g->rows == 0) return MOE_OK;
@@ -686,7 +685,6 @@ moe_status_t moe_grouped_matmul_int8(const moe_grouped_t* g, const void* a, cons
     MOE_TRY(need(w_scales));
     MOE_TRY(optional(offsets));
     MOE_TRY(need(c));
-    MOE_TRY(need_grouped_ws(*g, MOE_GROUPED_OP_INT8, ws, ws_bytes));
     clear_hip_error();
     MOE_LAUNCH(launch_grouped_int8(*g, a, a_scales, w, w_scales, offsets, c, static_cast<hipStream_t>(stream)));
     return MOE_OK;
