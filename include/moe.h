@@ -376,12 +376,13 @@ moe_status_t moe_expert_ffn_fp8(const moe_problem_t* p, const void* x, const int
  * is neither read nor written.  Offsets that break these rules give
  * unspecified values in the outputs, never an access outside the arrays.
  *
- * Limits (MOE_ERR_UNSUPPORTED otherwise): 1 <= E <= MOE_MAX_EXPERTS;
- * 0 <= rows <= 2^31 - 2^16; N and K at most MOE_GROUPED_MAX_DIM; every matrix
- * row a whole number of 16-byte words: N and K multiples of 8 (bf16) or of 4
- * (f32), for the 8-bit integer product K a multiple of 16 and N of 8; and
- * fewer than 2^24 - 2^11 output tiles (rows * max(N, K, 32) and E * N * K up
- * to 2^32 always fit).  Outputs must not overlap the inputs.
+ * Limits (MOE_ERR_UNSUPPORTED otherwise): 1 <= E <= MOE_MAX_EXPERTS; N and K
+ * at most MOE_GROUPED_MAX_DIM; every matrix row a whole number of 16-byte
+ * words: N and K multiples of 8 (bf16) or of 4 (f32), for the 8-bit integer
+ * product K a multiple of 16 and N of 8; and fewer than 2^24 - 2^11 output
+ * tiles: of 32 x 32, with a row tile begun for each queue, in c and da, and of
+ * 64 x 64 in dw.  Rows are below 2^29 by that; rows * max(N, K, 32) and
+ * E * N * K up to 2^32 always fit.  Outputs must not overlap the inputs.
  * Workspace: moe_grouped_workspace_size of the same problem; ws may be NULL
  * when that is 0.  Only a weight gradient ever needs one: for the forward and
  * the 8-bit integer product the size is 0, and their ws and ws_bytes are not

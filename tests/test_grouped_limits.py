@@ -53,3 +53,39 @@ def test_calls_that_need_no_workspace_reach_the_launch(lib):
         assert size(lib, g, L.MOE_GROUPED_OP_INT8) == (L.MOE_OK, 0)
         assert lib.moe_grouped_matmul(p, A, A, A, A, None, 0, None) == L.MOE_ERR_HIP
         assert lib.moe_grouped_matmul_int8(p, A, A, A, A, A, A, None, 0, None) == L.MOE_ERR_HIP
+
+
+# The most rows of one queue at the least width: one 32-row tile counts for
+# each 32 rows begun, and there may be fewer than 2^24 - 2^11 of them.
+MOST_ROWS = 32 * (2 ** 24 - 2 ** 11 - 1)
+
+
+@pytest.mark.parametrize("op", [1, 2, 3])
+@pytest.mark.parametrize("dtype", [L.MOE_DTYPE_BF16, L.MOE_DTYPE_F32])
+def test_the_most_rows(lib, op, dtype):
+    kw = dict(E=1, N=8, K=16 if op == 3 else 8, dtype=dtype)
+    assert size(lib, grp(rows=MOST_ROWS, **kw), op)[0] == L.MOE_OK
+    assert size(lib, grp(rows=MOST_ROWS + 1, **kw), op)[0] == UNS
+    # as many tiles in two columns
+    half = 32 * ((2 ** 24 - 2 ** 11) // 2 - 1)
+    kw["N"] = 40
+    assert size(lib, grp(rows=half, **kw), op)[0] == L.MOE_OK
+    assert size(lib, grp(rows=half + 1, **kw), op)[0] == UNS
+
+
+@pytest.mark.parametrize("rows", [2 ** 29, 2 ** 31 - 2 ** 16, 2 ** 31 - 2 ** 16 + 1, 2 ** 62, 2 ** 63 - 1])
+def test_more_rows_are_refused(lib, rows):
+    for op in (1, 2, 3):
+        for kw in (dict(N=8, K=16), dict(N=1 << 20, K=1 << 20)):
+            assert size(lib, grp(rows=rows, E=1, **kw), op)[0] == UNS
+
+
+@pytest.mark.parametrize("E", [1, 3, 256])
+def test_what_always_fits(lib, E):
+    """rows * max(N, K, 32) and E * N * K up to 2^32."""
+    for width in (16, 40, 64, 1000, 4096, 1 << 20):
+        rows = 2 ** 32 // max(width, 32)
+        for N, K in ((width, 16), (16, width)):
+            for dtype in (L.MOE_DTYPE_BF16, L.MOE_DTYPE_F32):
+                for op in (1, 2):
+                    assert size(lib, grp(rows=rows, E=E, N=N, K=K, dtype=dtype), op)[0] == L.MOE_OK, (rows, N, K)
