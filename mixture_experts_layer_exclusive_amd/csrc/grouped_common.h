@@ -5,6 +5,7 @@
 #include <type_traits>
 
 #include "device_util.h"
+#include "grouped_plan.h"
 #include "lds_dma.h"
 #include "moe_internal.h"
 
@@ -18,10 +19,7 @@ typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x16_t __attribute__((ext_vector_type(16)));
 
-constexpr int kNT = 0, kNN = 1, kTN = 2;
 constexpr int kBf16 = 0, kF32 = 1, kI8 = 2;
-constexpr int kXcds = 8;
-constexpr int kGroupM = 8;  // row tiles per group of the tile order
 
 // ---- queues and the tile order ---------------------------------------------
 
@@ -182,10 +180,8 @@ __device__ __forceinline__ void weight_tile_of(const Queues& q, int e, int part,
 // first.  Each XCD takes whole (parts of) queues, in a snake order, XCD 0 to 7
 // and back: their tiles read the same two operand blocks and share its L2
 // (dealing every expert's tiles over all XCDs: 128 queues of 2048 rows, 768 x
-// 2048, 970 us against 870).  With too few of them to keep the XCDs even, every
-// XCD takes an eighth of each expert's tiles instead.
-__host__ __device__ __forceinline__ bool whole_queues(int64_t queues) { return queues >= 32 || queues % kXcds == 0; }
-
+// 2048, 970 us against 870).  With too few of them to keep the XCDs even
+// (whole_queues), every XCD takes an eighth of each expert's tiles instead.
 __device__ __forceinline__ Found weight_tile(const Queues& q, int E, int M, int P, int bm, int bn, int qs, int parts,
                                              bool dealt, int xcd, int place, Tile& t) {
     const int whole = ((M + bm - 1) / bm) * ((P + bn - 1) / bn);
