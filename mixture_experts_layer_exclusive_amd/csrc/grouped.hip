@@ -31,8 +31,9 @@ namespace {
 // 8, and the slices of all its tiles are one stream: while a tile's last slices
 // are multiplied and its outputs stored, the first slices of the next are
 // landing.  (Weight gradients, whose tiles fall in cost: every other round is
-// dealt backwards, 128 queues of 2048 rows in the mean, uneven, 768 x 2048:
-// 813 us dealt one way, 793 so.)
+// dealt backwards.  16 uneven queues, 4096 rows in the mean, 1408 x 2048: 388
+// us, dealt one way 404; 24, 2048 in the mean, 2048 x 1024: 262 and 277; even
+// queues, and those dealt by load, the same either way.)
 //
 // Each slice has 4 steps of 32 bytes of q (16 bytes per half wave).  Step 0
 // multiplies fragments read during the slice before; the fragments of steps 1
@@ -45,9 +46,11 @@ namespace {
 // 28 1541, 36 1498, 52 1463).  Before step 3 the next slice has landed, and
 // step 3 reads its first fragments.
 //
-// The largest tiles at a long reduction are bound by power: the same product
-// over cached operands only, with one barrier per slice instead of two, or
-// with a part of its loads spread otherwise takes the same time to 1 %.
+// The largest tiles at a long reduction are bound by power first: products of
+// normal values from registers alone hold 1.8 GHz (16384 rows, 14336 x 4096:
+// 1045 us), of zeros 2.4 GHz (786 us), and this kernel 1.5 GHz.  One queue of
+// those rows takes 1358 us; 1334 over operands from the caches only, 1332
+// without half of the fragment reads.  8 queues of 2048: 1428, 1328, 1406.
 template <int MB, int NB, int NS, typename O>
 struct TileLds {
     static constexpr int STAGE = 64 * (MB + NB) * 128;
@@ -108,11 +111,11 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
     const int stride = blocks / kXcds;
     // weight gradients: how their tiles are dealt.  A stream's queues are uneven
     // if the longest is over 1.25 times the mean.  Few of them (below 32) then
-    // go over all XCDs (8 queues of 4096 rows in the mean, 4096 x 2048: 442 us, one
-    // queue to each XCD 557 us; with smaller tiles, whose problems are small, it
-    // changes nothing); more are dealt by load where the work is worth it: from
-    // half a slice per workgroup and expert (128 queues, 768 x 2048, of 512 rows,
-    // 96 slices: 259 us, in snake order 275; of 256 rows, 48 slices: 155 and 148).
+    // go over all XCDs (8 queues of 4096 rows in the mean, 4096 x 2048: 427 us,
+    // by load 557 us; with smaller tiles, whose problems are small, it changes
+    // nothing); more are dealt by load where the work is worth it: from half a
+    // slice per workgroup and expert (128 queues, 768 x 2048, of 512 rows, 96
+    // slices: 258 us, in snake order 273; of 256 rows, 48 slices, 151 either way).
     bool dealt = MODE == kTN && whole_queues(static_cast<int64_t>(E) * parts), uneven = false;
     Deal& deal = *reinterpret_cast<Deal*>(smem + (STREAM ? Lds::DEAL_AT : 0));
     const int tiles_of_queue = ((N + TM - 1) / TM) * ((K + TN - 1) / TN);
@@ -421,10 +424,11 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
                                  ? (static_cast<uint32_t>(r) * static_cast<uint32_t>(P) + c) * static_cast<uint32_t>(sizeof(O))
                                  : kOutOfRange;
                 }
-                // rows of whole 128-byte lines past the L2's lifetime (bf16, 16384 x
-                // 4864 x 128: 57 us, 61 through it); other rows' stores share
-                // lines, which the L2 has to put together (x 4904: 160 us past
-                // it, 67 through it)
+                // rows of whole 128-byte lines past the L2's lifetime (bf16, 65536 x
+                // 2048 x 256: 90 us, 97 through it; 16384 x 4864 x 128 and the large
+                // products the same to 1 %); other rows' stores share lines, which
+                // the L2 has to put together (16384 x 4904 x 128: 100 us past it, 42
+                // through it)
                 if (P % (128 / static_cast<int>(sizeof(O))) == 0) {
 #pragma unroll
                     for (int i = 0; i < 32 / RPS; ++i)

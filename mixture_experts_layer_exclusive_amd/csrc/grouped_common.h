@@ -115,8 +115,9 @@ __device__ __forceinline__ int quick_div(int a, int b) {
 // groups row tiles per column tile, so that the tiles running on one XCD at a
 // time share operand rows in its L2: kGroupM of them, or half as many for tiles
 // of 256 in at most 8 columns, so that the 32 workgroups of an XCD span whole
-// rows of C and read them once (bf16, 128 queues of 2048 rows, 2048 x 768: 798 us, in
-// groups of 8 861; 8 queues, 14336 x 4096, 56 columns: 1493 and 1468 us).
+// rows of C and read them once (bf16, 128 queues of 2048 rows, 2048 x 768: 788
+// us, in groups of 8 844; 8 queues, 14336 x 4096, 56 columns: in groups of 4
+// 1455 us, of 8 1434).
 __device__ __forceinline__ Found row_tile(const Queues& q, int E, int bm, int bn, int P, int xcd, int place,
                                           Tile& t) {
     const int total_m = __builtin_amdgcn_readfirstlane(q.end[E - 1]);
@@ -180,7 +181,7 @@ __device__ __forceinline__ void weight_tile_of(const Queues& q, int e, int part,
 // first.  Each XCD takes whole (parts of) queues, in a snake order, XCD 0 to 7
 // and back: their tiles read the same two operand blocks and share its L2
 // (dealing every expert's tiles over all XCDs: 128 queues of 2048 rows, 768 x
-// 2048, 970 us against 870).  With too few of them to keep the XCDs even
+// 2048, 747 us against 694).  With too few of them to keep the XCDs even
 // (whole_queues), every XCD takes an eighth of each expert's tiles instead.
 __device__ __forceinline__ Found weight_tile(const Queues& q, int E, int M, int P, int bm, int bn, int qs, int parts,
                                              bool dealt, int xcd, int place, Tile& t) {
@@ -213,8 +214,8 @@ __device__ __forceinline__ Found weight_tile(const Queues& q, int E, int M, int 
 // experts, longest first, each to the XCD that has the least so far; and of
 // an expert's `whole` tiles, one more to those of the XCD's `stride` (at most
 // 32) workgroups that have the least.  128 queues of 2048 rows in the mean, the
-// longest of 19000, 768 x 2048: 753 us, 822 us in the snake order; 64 queues,
-// 1408 x 2048: 1293 and 1436 us.  Filled by the first wave, the same in every
+// longest of 19000, 768 x 2048: 763 us, 829 us in the snake order; 64 queues of
+// 2560, the longest of 17000, 1408 x 2048: 896 and 1044 us.  Filled by the first wave, the same in every
 // workgroup, in 0.05 to 0.1 us per expert; costs are counted in slices, a tile's
 // start as two.  (Sums that overflow would only deal badly: the places stay a
 // permutation.)

@@ -32,13 +32,15 @@ constexpr int kTileN[kVariants] = {32, 64, 64, 128, 128, 256};
 // What a round of one tile per CU takes, in 10 ns: for every slice, and once
 // (start, epilogue), and no less than its stores.  Fitted to sweeps of rows,
 // queues and widths (E 1 to 128, rows per queue 1 to 1024, widths 768 to 4096);
-// on random problems the choice is within 5 % of the best variant in the mean.
+// on 361 random products the choice is 2.1 % slower than the best variant in the
+// mean, at worst 1.9x (a weight gradient with one queue of nine times the mean,
+// whose tiles of 256 last longest: the host does not know the queues' lengths).
 // A tile of a quarter the size takes more than a quarter of the time, so the
 // choice is between filling the last round and the rate within a round.  Both
-// sides, bf16: 8 queues of 512 rows, 4096 x 2048, tiles of 128 in 5 rounds 92 us,
-// tiles of 256 in 2 rounds 101 us; 64 queues of 512, 1408 x 2048, 13 rounds of
-// 128 243 us, 4 rounds of 256 224 us; one queue of 128 rows, 4096 x 4096, split
-// tiles of 32 in 2 rounds 16 us, tiles of 128 in one round 33 us.
+// sides, bf16: 8 queues of 512 rows, 4096 x 2048, tiles of 128 in 5 rounds 78 us,
+// tiles of 256 in 2 rounds 89 us; 64 queues of 512, 1408 x 2048, 13 rounds of
+// 128 239 us, 4 rounds of 256 208 us; one queue of 128 rows, 4096 x 4096, split
+// tiles of 32 in 2 rounds 17 us, tiles of 128 in one round 33 us.
 struct Cost {
     int slice, once;
 };
@@ -47,8 +49,8 @@ constexpr Cost kCost16[kVariants] = {{9, 100}, {25, 300}, {0, 0}, {30, 200}, {48
 // output as larger ones.
 constexpr Cost kCost32[kVariants] = {{17, 130}, {0, 0}, {50, 20}, {0, 0}, {0, 0}, {0, 0}};
 // Weight gradients of short queues are bound by their stores and starts (128
-// queues of 32 rows, 768 x 2048: float32 tiles of 64 516 us, of 128 374 us; bf16
-// tiles of 128 199 us, of 256 88 us).
+// queues of 32 rows, 768 x 2048: float32 tiles of 64 378 us, of 128 287 us, of
+// 256 225 us; bf16 tiles of 128 143 us, of 256 80 us).
 constexpr Cost kCostW16[kVariants] = {{0, 0}, {0, 0}, {0, 0}, {0, 0}, {53, 350}, {150, 500}};
 constexpr Cost kCostW32[kVariants] = {{0, 0}, {0, 0}, {50, 150}, {0, 0}, {195, 330}, {800, 600}};
 constexpr int kCus = 256;
@@ -148,9 +150,9 @@ int64_t workgroups(const moe_grouped_t& g, int mode, const Plan& p) {
 // CU's LDS, and not float32's 64 x 64 tiles with 128 x 128: of the former 4
 // workgroups fit a CU, of the pair 2 (16 queues of 256 rows, 512 x 1024: 113 us
 // together, 101 us one after the other).  Otherwise, together and one after the
-// other: bf16, 8 queues of 250 rows, 1000 x 520, 14.8 and 22.9 us; 17 of 289,
-// 648 x 304, 17.9 and 28.0 us; 8 of 1070, 552 x 1608, 65.7 and 66.6 us; one of 2
-// rows, 72 x 248, 5.2 and 8.7 us.
+// other: bf16, 8 queues of 250 rows, 1000 x 520, 14.2 and 20.6 us; 17 of 289,
+// 648 x 304, 17.5 and 23.6 us; 8 of 1070, 552 x 1608, 61.8 and 60.7 us; one of 2
+// rows, 72 x 248, 5.8 and 9.4 us.
 bool pairs(const moe_grouped_t& g, const Plan& pa, const Plan& pw) {
     return pa.v != kTile256 && pa.v != kSplit64 && pw.v != kTile256 && !(pa.v == kTile64 && pw.v == kTile128) &&
            workgroups(g, kNN, pa) + workgroups(g, kTN, pw) < (1 << 24);
