@@ -507,7 +507,7 @@ def _grouped_plan(op: int, rows: int, E: int, N: int, K: int, dtype):
 def grouped_workspace_size(op: int, rows: int, E: int, N: int, K: int, dtype) -> int:
     """Workspace bytes of a grouped product (``op``: 1 ``grouped_matmul``, 2
     ``grouped_matmul_backward``, 3 ``grouped_matmul_int8``, whose ``dtype``
-    is its output's)."""
+    is its output's).  0 for 1 and 3: their ``ws`` is checked, but not used."""
     return _grouped_plan(op, rows, E, N, K, dtype)[1]
 
 
