@@ -8,8 +8,10 @@
  * SwiGLU feed-forward over its queue; a gate-weighted combine returns the
  * results to token order.
  *
- * Beside it: the products by expert one at a time, with their gradients and
- * in 8-bit integers, for experts of another form (moe_grouped_*).
+ * Beside it: routing by scores, with a balance bias and groups of experts,
+ * and its gradient (moe_route_scored*); the combine's gradient; the products
+ * by expert one at a time, with their gradients, in 8-bit integers and in
+ * 4-bit floats, for experts of another form (moe_grouped_*).
  *
  * Sources (summaries of three papers; they give the structure, not the
  * formulas):
@@ -97,6 +99,28 @@ typedef enum {
     MOE_GROUPED_OP_BACKWARD = 2,
     MOE_GROUPED_OP_INT8 = 3
 } moe_grouped_op_t;
+
+/* What moe_route_scored makes of the logits. */
+typedef enum {
+    MOE_SCORE_SOFTMAX = 0, /* over all E experts */
+    MOE_SCORE_SIGMOID = 1  /* each expert by itself */
+} moe_score_t;
+
+/* Routing by scores: T tokens, E experts in `groups` equal groups of
+ * neighbours, of which the groups_kept best stay; k experts per token. */
+typedef struct {
+    int64_t T;
+    int32_t d;           /* hidden size and dtype (a moe_dtype_t value) of x and */
+    int32_t dtype;       /* w_router; not looked at when logits are given */
+    int32_t E;
+    int32_t k;
+    int32_t score;       /* a moe_score_t value */
+    int32_t groups;      /* 1: no groups */
+    int32_t groups_kept; /* groups: all stay */
+    int32_t group_top;   /* a group's value is the sum of its 1 or 2 best */
+    int32_t renormalise; /* nonzero: gates are shares of the chosen scores' sum */
+    float scale;         /* of the gates */
+} moe_gating_t;
 
 /* The problem statement: T tokens, hidden size d, E experts, top-k, SwiGLU
  * width f, storage dtype (a moe_dtype_t value). */
@@ -267,6 +291,77 @@ moe_status_t moe_expert_ffn(const moe_problem_t* p, const void* x_perm, const vo
  */
 moe_status_t moe_combine(const moe_problem_t* p, const void* y_perm, const int32_t* assign_pos,
                          const float* topk_gates, void* y, void* stream);
+
+/*
+ * moe_combine_backward -- the gradients of moe_combine for the output
+ * gradient dy [T, d], for a layer made of parts:
+ *   dy_perm[assign_pos[t*k + j], :] = topk_gates[t, j] * dy[t, :]   (one rounding)
+ *   dgates[t, j] = sum_c dy[t, c] * y_perm[assign_pos[t*k + j], c]  (fp32)
+ * Either of dy_perm [T*k, d] and dgates [T, k] may be NULL (then it is not
+ * computed, and without dgates y_perm may be NULL), not both.  A negative
+ * position stands for an expert elsewhere, as in moe_combine: nothing is
+ * written to dy_perm for it, and its dgates is 0.  Positions below T*k must
+ * differ; larger ones count as negative.  dy_perm must not overlap the
+ * inputs.  No atomics: the same inputs give the same bits.
+ */
+moe_status_t moe_combine_backward(const moe_problem_t* p, const void* dy, const void* y_perm,
+                                  const int32_t* assign_pos, const float* topk_gates, void* dy_perm, float* dgates,
+                                  void* stream);
+
+/* Bytes of device workspace moe_route_scored needs when it writes
+ * score_sums (without them it needs none).  Host only; no HIP call. */
+moe_status_t moe_route_scored_workspace_size(const moe_gating_t* g, size_t* bytes);
+
+/*
+ * moe_route_scored -- moe_route with a score for every expert, a bias that
+ * balances the load, and groups (the router: Piper, Japanese explainer,
+ * opening section; skewed loads: Piper technical summary, section 1; the
+ * scheme is this library's reading):
+ *   s[t, e] = softmax over e of logits[t, :], or sigmoid(logits[t, e])
+ *   c[t, e] = s[t, e] + bias[e]          (bias [E] float32, NULL: zeros)
+ *   groups: expert e lies in group e / (E / groups), whose value is the sum
+ *     of its group_top largest c (of all, if it has fewer); the experts of the
+ *     groups_kept groups of the largest values stay.
+ *   topk_ids[t, j]: the k largest c of those, in descending order.
+ *   topk_gates[t, j] = scale * s / (sum of the chosen s), or scale * s
+ *     without renormalise: the bias decides who is chosen, not how much.
+ *   score_sums[e] = sum_t s[t, e]        (float32 [E], optional: what losses
+ *     that balance the load are made of)
+ * Equal c, and equal values of groups, go to the lower index.  c is taken
+ * in 64 bits (experts whose c differ by less than that resolves may come in
+ * either order); without a bias, and without sums over a group, the order is
+ * that of the logits.  Scores below 2^-126 may count as 0; chosen scores
+ * that are all 0 give gates of 0.  A logit of minus infinity has the score
+ * 0, also where all of a token's are (then all scores are 0).  A NaN, in a
+ * logit or the bias, is chosen last, and the gates it enters are NaN.
+ * Whatever the inputs, a token's ids are k different experts.
+ * logits_in, x, w_router and logits_out as in moe_route (bf16 needs d to be
+ * a multiple of 64 there).  Limits: E and k as everywhere, T <= 2^24 - 1 and
+ * T*k <= 2^31 - 1; groups divides E, and k <= groups_kept * (E / groups).
+ * Workspace: moe_route_scored_workspace_size if score_sums is given, else not
+ * looked at.  T = 0 writes zeros to score_sums and nothing else.  No atomics:
+ * the same inputs give the same bits.
+ */
+moe_status_t moe_route_scored(const moe_gating_t* g, const void* x, const void* w_router, const float* logits_in,
+                              float* logits_out, const float* bias, int32_t* topk_ids, float* topk_gates,
+                              float* score_sums, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_route_scored_backward -- the gradient of moe_route_scored by its logits
+ * [T, E], with the choice held fixed, for the gradients dgates [T, k] of the
+ * gates and dscore_sums [E] of the score sums (NULL: zeros):
+ *   ds[t, e] = dscore_sums[e] + (e chosen in slot j) scale *
+ *     (renormalise ? (dgates[t, j] - sum_i r_i dgates[t, i]) / S : dgates[t, j])
+ *     with S = sum of the chosen s and r_i = s_i / S (all 0 if S is 0)
+ *   sigmoid: dlogits = ds s (1 - s);  softmax: dlogits = s (ds - sum_i s_i ds_i)
+ * dlogits [T, E] of dlogits_dtype (a moe_dtype_t value), arithmetic in fp32.
+ * The bias has no gradient, and groups do not matter here.  The router's
+ * gradients are those of moe_grouped_matmul with one queue of all tokens.  T = 0
+ * is a no-op.
+ */
+moe_status_t moe_route_scored_backward(const moe_gating_t* g, const float* logits, const int32_t* topk_ids,
+                                       const float* dgates, const float* dscore_sums, int32_t dlogits_dtype,
+                                       void* dlogits, void* stream);
 
 /*
  * moe_forward -- the whole layer on one stream with no host
@@ -448,6 +543,50 @@ moe_status_t moe_quantize_rows_int8(const void* src, int64_t rows, int32_t cols,
 moe_status_t moe_grouped_matmul_int8(const moe_grouped_t* g, const void* a, const float* a_scales, const void* w,
                                      const float* w_scales, const int32_t* offsets, void* c, void* ws,
                                      size_t ws_bytes, void* stream);
+
+/*
+ * moe_quantize_rows_mxfp4 -- 4-bit microscaled floats (OCP MX: MXFP4) of a
+ * matrix src [rows, cols] (dtype: a moe_dtype_t value), one power of two per
+ * block of 32 values of a row:
+ *   scale = 2^(floor(log2(max |block|)) - 2), at least 2^-127
+ *   code  = sign | index of |x| / scale rounded to one of 0, 0.5, 1, 1.5, 2, 3,
+ *           4, 6 (to nearest, ties to the even index; above 6 becomes 6)
+ * codes [rows, cols / 2]: two to a byte, the even column in the low half.
+ * scales [ceil(cols / 256), rows, 8]: the exponent + 127 of block b of row r
+ * at [b / 8, r, b % 8], so that the product reads what belongs to a tile's
+ * slice in one piece; the bytes of blocks past the row are 127.  An all-zero
+ * block has the scale 1.  A block with a NaN or an infinity has the scale byte
+ * 255, which stands for NaN, and codes 0: products with it are NaN.  cols
+ * must be a positive multiple of 32, at most MOE_GROUPED_MAX_DIM, rows at most
+ * 2^24 - 1 and rows * cols at most 2^35 - 2^11 (MOE_ERR_UNSUPPORTED
+ * otherwise).  rows = 0 is a no-op.
+ */
+moe_status_t moe_quantize_rows_mxfp4(const void* src, int64_t rows, int32_t cols, int32_t dtype, void* codes,
+                                     void* scales, void* stream);
+
+/*
+ * moe_dequantize_rows_mxfp4 -- the numbers that codes and scales stand for,
+ * dst [rows, cols] of `dtype`: exact but for overflow to infinity (scales
+ * above 2^125).  Limits as for moe_quantize_rows_mxfp4.
+ */
+moe_status_t moe_dequantize_rows_mxfp4(const void* codes, const void* scales, int64_t rows, int32_t cols,
+                                       int32_t dtype, void* dst, void* stream);
+
+/*
+ * moe_grouped_matmul_mxfp4 -- moe_grouped_matmul of 4-bit microscaled floats:
+ * for every expert e and row r of its queue
+ *   c[r, n] = sum_k a[r, k] * w[e, n, k]
+ * a [rows, K / 2] codes with a_scales [ceil(K / 256), rows, 8], w [E, N, K / 2]
+ * with w_scales [ceil(K / 256), E, N, 8] (moe_quantize_rows_mxfp4 makes both;
+ * the scale bytes of blocks past K do not matter), c [rows, N] of the
+ * problem's dtype.  Products are exact, accumulation is fp32 on the
+ * block-scaled MFMA, then one rounding to the dtype.  K must be a multiple
+ * of 32 and N of 8 (MOE_ERR_UNSUPPORTED otherwise).  offsets = NULL: a dense
+ * product, every row with the one matrix w [N, K / 2] (E must be 1).  rows =
+ * 0 is a no-op.  No workspace.
+ */
+moe_status_t moe_grouped_matmul_mxfp4(const moe_grouped_t* g, const void* a, const void* a_scales, const void* w,
+                                      const void* w_scales, const int32_t* offsets, void* c, void* stream);
 
 /*
  * moe_mfma_peak -- measurement kernel, not part of the layer: `workgroups`

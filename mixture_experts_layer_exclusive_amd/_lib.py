@@ -32,6 +32,9 @@ MOE_GROUPED_OP_MATMUL = 1
 MOE_GROUPED_OP_BACKWARD = 2
 MOE_GROUPED_OP_INT8 = 3
 
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+
 MOE_MAX_EXPERTS = 256
 MOE_MAX_TOPK = 32
 MOE_NO_ALLOC_SCRATCH_BYTES = 1 << 20
@@ -50,6 +53,12 @@ class MoeProblem(ctypes.Structure):
 
 class MoeGrouped(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("E", _i32), ("N", _i32), ("K", _i32), ("dtype", _i32)]
+
+
+class MoeGating(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("d", _i32), ("dtype", _i32), ("E", _i32), ("k", _i32), ("score", _i32),
+                ("groups", _i32), ("groups_kept", _i32), ("group_top", _i32), ("renormalise", _i32),
+                ("scale", ctypes.c_float)]
 
 
 class MoeForwardOutputs(ctypes.Structure):
@@ -74,6 +83,7 @@ class MoeBackwardOutputs(ctypes.Structure):
 
 _PP = ctypes.POINTER(MoeProblem)
 _PG = ctypes.POINTER(MoeGrouped)
+_PR = ctypes.POINTER(MoeGating)
 
 SIGNATURES = {
     "moe_status_string": (ctypes.c_char_p, [_i32]),
@@ -99,6 +109,13 @@ SIGNATURES = {
     "moe_grouped_matmul_backward": (_i32, [_PG, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
     "moe_quantize_rows_int8": (_i32, [_p, ctypes.c_int64, _i32, _i32, _p, _p, _p]),
     "moe_grouped_matmul_int8": (_i32, [_PG, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
+    "moe_combine_backward": (_i32, [_PP, _p, _p, _p, _p, _p, _p, _p]),
+    "moe_route_scored_workspace_size": (_i32, [_PR, ctypes.POINTER(_sz)]),
+    "moe_route_scored": (_i32, [_PR, _p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
+    "moe_route_scored_backward": (_i32, [_PR, _p, _p, _p, _p, _i32, _p, _p]),
+    "moe_quantize_rows_mxfp4": (_i32, [_p, ctypes.c_int64, _i32, _i32, _p, _p, _p]),
+    "moe_dequantize_rows_mxfp4": (_i32, [_p, _p, ctypes.c_int64, _i32, _i32, _p, _p]),
+    "moe_grouped_matmul_mxfp4": (_i32, [_PG, _p, _p, _p, _p, _p, _p, _p]),
 }
 
 _lib = None

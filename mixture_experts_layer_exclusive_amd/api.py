@@ -146,6 +146,115 @@ def route(k: int, x: Optional[torch.Tensor] = None, w_router: Optional[torch.Ten
     return ids, gates, logits_out
 
 
+_SCORES = {"softmax": L.MOE_SCORE_SOFTMAX, "sigmoid": L.MOE_SCORE_SIGMOID}
+
+
+def _gating(T: int, E: int, k: int, score: str, groups: int, groups_kept: Optional[int], group_top: int,
+            renormalise: bool, scale: float, d: int = 1, dtype=torch.float32) -> L.MoeGating:
+    if score not in _SCORES:
+        raise ValueError(f"score {score!r}, expected 'softmax' or 'sigmoid'")
+    return L.MoeGating(T=T, d=d, dtype=_DTYPES[dtype], E=E, k=k, score=_SCORES[score], groups=groups,
+                       groups_kept=groups if groups_kept is None else groups_kept, group_top=group_top,
+                       renormalise=1 if renormalise else 0, scale=scale)
+
+
+def route_scored(k: int, x: Optional[torch.Tensor] = None, w_router: Optional[torch.Tensor] = None,
+                 logits: Optional[torch.Tensor] = None, score: str = "softmax",
+                 bias: Optional[torch.Tensor] = None, groups: int = 1, groups_kept: Optional[int] = None,
+                 group_top: int = 2, renormalise: bool = True, scale: float = 1.0, with_score_sums: bool = False,
+                 ids: Optional[torch.Tensor] = None, gates: Optional[torch.Tensor] = None,
+                 logits_out: Optional[torch.Tensor] = None, score_sums: Optional[torch.Tensor] = None,
+                 ws: Optional[torch.Tensor] = None):
+    """``route`` with a score for every expert: softmax over the experts, or
+    sigmoid.  The k experts of the largest score + ``bias`` (fp32 [E]: balances
+    the load, does not enter the gates) are chosen, of the ``groups_kept`` best
+    of ``groups`` equal groups of neighbours (a group's value: the sum of its
+    ``group_top`` (1 or 2) best; ``groups_kept`` None: all stay).  Gates are
+    ``scale`` times the chosen scores, divided by their sum with
+    ``renormalise``.  Returns (topk_ids int32 [T, k], topk_gates fp32 [T, k],
+    logits fp32 [T, E]), and with ``with_score_sums`` a fourth: the scores'
+    sums over the tokens, fp32 [E], for losses that balance the load."""
+    if logits is not None:
+        if logits.dim() != 2:
+            raise ValueError("logits must be [T, E]")
+        T, E = logits.shape
+        dev, d, dt = logits.device, 1, torch.float32
+        _expect("logits", logits, (T, E), torch.float32)
+        x = w_router = None
+        logits_out = logits
+    else:
+        if x is None or w_router is None or x.dim() != 2 or w_router.dim() != 2:
+            raise ValueError("without logits, x [T, d] and w_router [E, d] are required")
+        T, d = x.shape
+        E = w_router.shape[0]
+        dev = x.device
+        dt = _float_dtype("x", x)
+        _expect("x", x, (T, d), dt)
+        _expect("w_router", w_router, (E, d), dt, dev)
+        _expect("logits_out", logits_out, (T, E), torch.float32, dev, required=False)
+        if logits_out is None:
+            logits_out = torch.empty((T, E), dtype=torch.float32, device=dev)
+    _expect("bias", bias, (E,), torch.float32, dev, required=False)
+    _expect("ids", ids, (T, k), torch.int32, dev, required=False)
+    _expect("gates", gates, (T, k), torch.float32, dev, required=False)
+    _expect("score_sums", score_sums, (E,), torch.float32, dev, required=False)
+    _expect_ws(ws, dev)
+    g = _gating(T, E, k, score, groups, groups_kept, group_top, renormalise, scale, d, dt)
+    nbytes = 0
+    if with_score_sums:
+        if score_sums is None:
+            score_sums = torch.empty((E,), dtype=torch.float32, device=dev)
+        if ws is None:
+            ws = torch.empty((max(route_scored_workspace_size(g), 256),), dtype=torch.uint8, device=dev)
+        nbytes = ws.numel() * ws.element_size()
+    if ids is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    if gates is None:
+        gates = torch.empty((T, k), dtype=torch.float32, device=dev)
+    ptrs = (_addr(x), _addr(w_router), _addr(logits), None if logits is not None else _addr(logits_out), _addr(bias),
+            _addr(ids), _addr(gates), _addr(score_sums) if with_score_sums else None,
+            _addr(ws) if with_score_sums else None)
+    if T > 0 or with_score_sums:
+        _launch(dev, "moe_route_scored", L.load().moe_route_scored, ctypes.byref(g), *ptrs, nbytes)
+    return (ids, gates, logits_out, score_sums) if with_score_sums else (ids, gates, logits_out)
+
+
+def route_scored_workspace_size(g: L.MoeGating) -> int:
+    """Workspace bytes of ``route_scored`` with score sums."""
+    n = ctypes.c_size_t(0)
+    L.check(L.load().moe_route_scored_workspace_size(ctypes.byref(g), ctypes.byref(n)),
+            "moe_route_scored_workspace_size")
+    return n.value
+
+
+def route_scored_backward(logits: torch.Tensor, topk_ids: torch.Tensor, dgates: torch.Tensor,
+                          score: str = "softmax", renormalise: bool = True, scale: float = 1.0,
+                          dscore_sums: Optional[torch.Tensor] = None, dtype=torch.float32,
+                          dlogits: Optional[torch.Tensor] = None):
+    """Gradient of ``route_scored`` by its logits, with the choice held fixed:
+    dlogits [T, E] of ``dtype`` (fp32 or bf16) for dgates fp32 [T, k] and
+    dscore_sums fp32 [E] (None: zeros).  The router's gradients follow from
+    ``grouped_matmul_backward(x, w_router[None], [0, T], dlogits)``."""
+    if logits.dim() != 2 or topk_ids.dim() != 2:
+        raise ValueError("logits must be [T, E] and topk_ids [T, k]")
+    if dtype not in _DTYPES:
+        raise ValueError(f"dtype {dtype}, expected float32 or bfloat16")
+    T, E = logits.shape
+    k = topk_ids.shape[1]
+    dev = logits.device
+    _expect("logits", logits, (T, E), torch.float32)
+    _expect("topk_ids", topk_ids, (T, k), torch.int32, dev)
+    _expect("dgates", dgates, (T, k), torch.float32, dev)
+    _expect("dscore_sums", dscore_sums, (E,), torch.float32, dev, required=False)
+    _expect("dlogits", dlogits, (T, E), dtype, dev, required=False)
+    if dlogits is None:
+        dlogits = torch.empty((T, E), dtype=dtype, device=dev)
+    g = _gating(T, E, k, score, 1, None, 1, renormalise, scale)
+    ptrs = (_addr(logits), _addr(topk_ids), _addr(dgates), _addr(dscore_sums), _DTYPES[dtype], _addr(dlogits))
+    _launch(dev, "moe_route_scored_backward", L.load().moe_route_scored_backward, ctypes.byref(g), *ptrs)
+    return dlogits
+
+
 def dispatch(topk_ids: torch.Tensor, E: int, x: Optional[torch.Tensor] = None,
              with_x_perm: bool = False, ws: Optional[torch.Tensor] = None,
              out: Optional[dict] = None) -> dict:
@@ -278,6 +387,45 @@ def combine(y_perm: torch.Tensor, assign_pos: torch.Tensor, gates: torch.Tensor,
     L.check(L.load().moe_combine(ctypes.byref(p), _ptr(y_perm), _ptr(assign_pos), _ptr(gates),
                                  _ptr(y), _stream(dev)), "moe_combine")
     return y
+
+
+def combine_backward(dy: torch.Tensor, assign_pos: torch.Tensor, gates: torch.Tensor,
+                     y_perm: Optional[torch.Tensor] = None, with_dy_perm: bool = True, with_dgates: bool = True,
+                     out: Optional[dict] = None) -> dict:
+    """Gradients of ``combine`` for dy [T, d]: dy_perm [T*k, d] (rows that no
+    position names are not written) and dgates fp32 [T, k], each None when not
+    asked for.  y_perm is needed for dgates only.  ``out`` may supply either
+    tensor."""
+    if not (with_dy_perm or with_dgates):
+        raise ValueError("with_dy_perm or with_dgates is required")
+    if with_dgates and y_perm is None:
+        raise ValueError("y_perm is required for dgates")
+    if gates.dim() != 2 or dy.dim() != 2:
+        raise ValueError("gates must be [T, k] and dy [T, d]")
+    T, k = gates.shape
+    d = dy.shape[1]
+    dev = dy.device
+    dt = _float_dtype("dy", dy)
+    _expect("dy", dy, (T, d), dt)
+    _expect("y_perm", y_perm, (T * k, d), dt, dev, required=False)
+    _expect("assign_pos", assign_pos, (T * k,), torch.int32, dev)
+    _expect("gates", gates, (T, k), torch.float32, dev)
+    res = dict(out or {})
+    _expect("dy_perm", res.get("dy_perm"), (T * k, d), dt, dev, required=False)
+    _expect("dgates", res.get("dgates"), (T, k), torch.float32, dev, required=False)
+    if not with_dy_perm:
+        res["dy_perm"] = None
+    elif res.get("dy_perm") is None:
+        res["dy_perm"] = torch.empty((T * k, d), dtype=dt, device=dev)
+    if not with_dgates:
+        res["dgates"] = None
+    elif res.get("dgates") is None:
+        res["dgates"] = torch.empty((T, k), dtype=torch.float32, device=dev)
+    p = problem(T, d, k, k, 64, dt)
+    ptrs = (_addr(dy), _addr(y_perm) if with_dgates else None, _addr(assign_pos), _addr(gates), _addr(res["dy_perm"]),
+            _addr(res["dgates"]))
+    _launch(dev, "moe_combine_backward", L.load().moe_combine_backward, ctypes.byref(p), *ptrs)
+    return res
 
 
 def forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
@@ -643,6 +791,91 @@ def grouped_matmul_int8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor
     g, ws, nbytes = _grouped(L.MOE_GROUPED_OP_INT8, R, E, N, K, out_dtype, dev, ws)
     ptrs = (_addr(a), _addr(a_scales), _addr(w), _addr(w_scales), _addr(offsets), _addr(c), _addr(ws))
     _launch(dev, "moe_grouped_matmul_int8", L.load().moe_grouped_matmul_int8, g, *ptrs, nbytes)
+    return c
+
+
+def _mxfp4_slices(cols: int) -> int:
+    return (cols + 255) // 256
+
+
+def quantize_rows_mxfp4(src: torch.Tensor, codes: Optional[torch.Tensor] = None,
+                        scales: Optional[torch.Tensor] = None):
+    """4-bit microscaled floats (OCP MXFP4) of a bf16 or fp32 matrix [rows,
+    cols], cols a multiple of 32: codes uint8 [rows, cols / 2], two to a byte,
+    the even column in the low half, and scales uint8 [ceil(cols / 256), rows,
+    8], the power of two + 127 of block b (32 columns) of row r at [b // 8, r,
+    b % 8].  A matrix of E experts' weights is ``w.view(E * N, K)``; scales kept
+    as [rows, cols / 32] elsewhere are padded to a multiple of 8 columns and
+    come into this order by ``.view(rows, -1, 8).transpose(0, 1).contiguous()``."""
+    if src.dim() != 2:
+        raise ValueError("src must be [rows, cols]")
+    rows, cols = src.shape
+    dev = src.device
+    dt = _float_dtype("src", src)
+    _expect("src", src, (rows, cols), dt)
+    if codes is None:
+        codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev)
+    else:
+        _expect("codes", codes, (rows, cols // 2), torch.uint8, dev)
+    if scales is None:
+        scales = torch.empty((_mxfp4_slices(cols), rows, 8), dtype=torch.uint8, device=dev)
+    else:
+        _expect("scales", scales, (_mxfp4_slices(cols), rows, 8), torch.uint8, dev)
+    ptrs = (_addr(src), rows, cols, _DTYPES[dt], _addr(codes), _addr(scales))
+    _launch(dev, "moe_quantize_rows_mxfp4", L.load().moe_quantize_rows_mxfp4, *ptrs)
+    return codes, scales
+
+
+def dequantize_rows_mxfp4(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.bfloat16,
+                          out: Optional[torch.Tensor] = None):
+    """The numbers that ``quantize_rows_mxfp4``'s codes and scales stand for:
+    [rows, cols] of ``dtype`` (bf16 or fp32; exact in both)."""
+    if codes.dim() != 2:
+        raise ValueError("codes must be [rows, cols / 2]")
+    if dtype not in _DTYPES:
+        raise ValueError(f"dtype {dtype}, expected float32 or bfloat16")
+    rows, cols = codes.shape[0], 2 * codes.shape[1]
+    dev = codes.device
+    _expect("codes", codes, (rows, cols // 2), torch.uint8)
+    _expect("scales", scales, (_mxfp4_slices(cols), rows, 8), torch.uint8, dev)
+    if out is None:
+        out = torch.empty((rows, cols), dtype=dtype, device=dev)
+    else:
+        _expect("out", out, (rows, cols), dtype, dev)
+    ptrs = (_addr(codes), _addr(scales), rows, cols, _DTYPES[dtype], _addr(out))
+    _launch(dev, "moe_dequantize_rows_mxfp4", L.load().moe_dequantize_rows_mxfp4, *ptrs)
+    return out
+
+
+def grouped_matmul_mxfp4(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                         offsets: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
+                         c: Optional[torch.Tensor] = None):
+    """``grouped_matmul`` of 4-bit microscaled floats (``quantize_rows_mxfp4``):
+    a uint8 [R, K / 2] with a_scales [S, R, 8], w uint8 [E, N, K / 2] with
+    w_scales [S, E, N, 8], S = ceil(K / 256); returns c [R, N] of
+    ``out_dtype``.  Without offsets the product is dense: w [N, K / 2], w_scales
+    [S, N, 8]."""
+    if a.dim() != 2 or w.dim() != (2 if offsets is None else 3):
+        raise ValueError("a must be [R, K / 2] and w [E, N, K / 2] ([N, K / 2] without offsets)")
+    if out_dtype not in _DTYPES:
+        raise ValueError(f"out_dtype {out_dtype}, expected float32 or bfloat16")
+    R, half = a.shape
+    E = 1 if offsets is None else w.shape[0]
+    N = w.shape[-2]
+    S = _mxfp4_slices(2 * half)
+    dev = a.device
+    _expect("a", a, (R, half), torch.uint8)
+    _expect("a_scales", a_scales, (S, R, 8), torch.uint8, dev)
+    _expect("w", w, w.shape[:-1] + (half,), torch.uint8, dev)
+    _expect("w_scales", w_scales, (S, *w.shape[:-1], 8), torch.uint8, dev)
+    _expect("offsets", offsets, (E + 1,), torch.int32, dev, required=False)
+    if c is None:
+        c = torch.empty((R, N), dtype=out_dtype, device=dev)
+    else:
+        _expect("c", c, (R, N), out_dtype, dev)
+    g = L.MoeGrouped(rows=R, E=E, N=N, K=2 * half, dtype=_DTYPES[out_dtype])
+    ptrs = (_addr(a), _addr(a_scales), _addr(w), _addr(w_scales), _addr(offsets), _addr(c))
+    _launch(dev, "moe_grouped_matmul_mxfp4", L.load().moe_grouped_matmul_mxfp4, ctypes.byref(g), *ptrs)
     return c
 
 

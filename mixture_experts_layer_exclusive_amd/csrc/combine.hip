@@ -4,6 +4,10 @@
 // k expert rows of its token and accumulates in fp32 in ascending j, then
 // rounds once.  Every y row is written exactly once, so the result does not
 // depend on scheduling.
+//
+// And its gradient:
+//   dy_perm[assign_pos[t*k + j], :] = gates[t, j] * dy[t, :]
+//   dgates[t, j] = sum_c dy[t, c] * y_perm[assign_pos[t*k + j], c]
 #include "device_util.h"
 #include "moe_internal.h"
 
@@ -105,7 +109,122 @@ __global__ __launch_bounds__(256) void combine_f32_kernel(const float* __restric
     }
 }
 
+// ---- the gradient --------------------------------------------------------------
+//
+// One workgroup per token: a thread keeps its columns of dy, and of KM slots at a
+// time reads y_perm's rows, adds to the slots' products and writes dy_perm's rows.
+// The products' sums over the workgroup are taken at the end, in a fixed order.
+template <typename T, int V>
+struct Chunk;  // V values
+template <>
+struct Chunk<bf16_t, 8> {
+    using Raw = uint4;
+    static __device__ __forceinline__ void unpack(const uint4& w, float (&v)[8]) {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = lo_bf16(u[i]);
+            v[2 * i + 1] = hi_bf16(u[i]);
+        }
+    }
+    static __device__ __forceinline__ uint4 scaled(const float (&v)[8], float g) {
+        return make_uint4(pack_bf16x2(g * v[0], g * v[1]), pack_bf16x2(g * v[2], g * v[3]),
+                          pack_bf16x2(g * v[4], g * v[5]), pack_bf16x2(g * v[6], g * v[7]));
+    }
+};
+template <>
+struct Chunk<float, 4> {
+    using Raw = float4;
+    static __device__ __forceinline__ void unpack(const float4& w, float (&v)[4]) {
+        v[0] = w.x;
+        v[1] = w.y;
+        v[2] = w.z;
+        v[3] = w.w;
+    }
+    static __device__ __forceinline__ float4 scaled(const float (&v)[4], float g) {
+        return make_float4(g * v[0], g * v[1], g * v[2], g * v[3]);
+    }
+};
+template <>
+struct Chunk<float, 1> {
+    using Raw = float;
+    static __device__ __forceinline__ void unpack(const float& w, float (&v)[1]) { v[0] = w; }
+    static __device__ __forceinline__ float scaled(const float (&v)[1], float g) { return g * v[0]; }
+};
+
+template <typename T, int V, int KM>
+__global__ __launch_bounds__(256) void combine_backward_kernel(
+    const typename Chunk<T, V>::Raw* __restrict__ dy, const typename Chunk<T, V>::Raw* __restrict__ y_perm,
+    const int32_t* __restrict__ assign_pos, const float* __restrict__ gates, int k, int n, int chunks,
+    typename Chunk<T, V>::Raw* __restrict__ dy_perm, float* __restrict__ dgates) {
+    using C = Chunk<T, V>;
+    __shared__ float s_dot[4][KM];
+    const int64_t t = blockIdx.x;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int j0 = 0; j0 < k; j0 += KM) {
+        int pos[KM];
+        float g[KM], dot[KM];
+#pragma unroll
+        for (int j = 0; j < KM; ++j) {
+            pos[j] = j0 + j < k ? assign_pos[t * k + j0 + j] : -1;
+            if (pos[j] >= n) pos[j] = -1;
+            g[j] = j0 + j < k ? gates[t * k + j0 + j] : 0.f;
+            dot[j] = 0.f;
+        }
+        for (int c = threadIdx.x; c < chunks; c += 256) {
+            float a[V];
+            C::unpack(dy[t * chunks + c], a);
+#pragma unroll
+            for (int j = 0; j < KM; ++j) {
+                if (pos[j] < 0) continue;
+                const int64_t at = static_cast<int64_t>(pos[j]) * chunks + c;
+                if (dgates != nullptr) {
+                    float b[V];
+                    C::unpack(y_perm[at], b);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) dot[j] = fmaf(a[i], b[i], dot[j]);
+                }
+                if (dy_perm != nullptr) dy_perm[at] = C::scaled(a, g[j]);
+            }
+        }
+        if (dgates == nullptr) continue;
+#pragma unroll
+        for (int j = 0; j < KM; ++j) {
+#pragma unroll
+            for (int off = 32; off > 0; off >>= 1) dot[j] += __shfl_xor(dot[j], off, 64);
+            if (lane == 0) s_dot[wave][j] = dot[j];
+        }
+        __syncthreads();
+        if (threadIdx.x < KM && j0 + threadIdx.x < k)
+            dgates[t * k + j0 + threadIdx.x] = (s_dot[0][threadIdx.x] + s_dot[1][threadIdx.x]) +
+                                               (s_dot[2][threadIdx.x] + s_dot[3][threadIdx.x]);
+        __syncthreads();
+    }
+}
+
+template <typename T, int V>
+hipError_t start_combine_backward(const moe_problem_t& p, const void* dy, const void* y_perm,
+                                  const int32_t* assign_pos, const float* gates, void* dy_perm, float* dgates,
+                                  hipStream_t s) {
+    using Raw = typename Chunk<T, V>::Raw;
+    const unsigned grid = static_cast<unsigned>(p.T);
+    const int n = static_cast<int>(p.T * p.k);
+    combine_backward_kernel<T, V, 4><<<grid, 256, 0, s>>>(static_cast<const Raw*>(dy), static_cast<const Raw*>(y_perm),
+                                                          assign_pos, gates, p.k, n, p.d / V,
+                                                          static_cast<Raw*>(dy_perm), dgates);
+    return hipGetLastError();
+}
+
 }  // namespace
+
+hipError_t launch_combine_backward(const moe_problem_t& p, const void* dy, const void* y_perm,
+                                   const int32_t* assign_pos, const float* gates, void* dy_perm, float* dgates,
+                                   hipStream_t s) {
+    if (p.dtype == MOE_DTYPE_BF16)
+        return start_combine_backward<bf16_t, 8>(p, dy, y_perm, assign_pos, gates, dy_perm, dgates, s);
+    if (p.d % 4 == 0) return start_combine_backward<float, 4>(p, dy, y_perm, assign_pos, gates, dy_perm, dgates, s);
+    return start_combine_backward<float, 1>(p, dy, y_perm, assign_pos, gates, dy_perm, dgates, s);
+}
 
 hipError_t launch_combine(const moe_problem_t& p, const void* y_perm, const int32_t* assign_pos,
                           const float* gates, void* y, hipStream_t s) {

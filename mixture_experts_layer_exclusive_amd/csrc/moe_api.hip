@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <mutex>
 
 #include "moe.h"
@@ -22,7 +23,7 @@ static __device__ __align__(256) int32_t scratch[MOE_NO_ALLOC_SCRATCH_BYTES / 4]
 
 namespace {
 
-constexpr int32_t kAbiVersion = 4;
+constexpr int32_t kAbiVersion = 5;
 constexpr size_t kAlign = 256;
 
 bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
@@ -162,26 +163,61 @@ size_t forward_ws(const moe_problem_t& p) {
     return b;
 }
 
+// What the operands of a grouped product are.
+enum class Codes { kNone, kInt8, kMxfp4 };
+
 // Limits of the grouped products: rows of whole 16-byte words (int8: codes of
-// K bytes), tile rows addressed with 32-bit byte offsets, 32-bit work-item
-// counts.
-moe_status_t check_grouped(const moe_grouped_t* g, bool int8) {
+// K bytes, 4-bit floats: of K / 2), tile rows addressed with 32-bit byte
+// offsets, 32-bit work-item counts.
+moe_status_t check_grouped(const moe_grouped_t* g, Codes codes) {
     if (g == nullptr) return MOE_ERR_INVALID_ARGUMENT;
     if (g->rows < 0 || g->E < 1 || g->N < 1 || g->K < 1) return MOE_ERR_INVALID_ARGUMENT;
     if (g->dtype != MOE_DTYPE_F32 && g->dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARGUMENT;
     // (row numbers past a matrix's end, by less than a tile, stay within int32)
     if (g->E > MOE_MAX_EXPERTS || g->rows > INT32_MAX - 0xffff) return MOE_ERR_UNSUPPORTED;
     if (g->N > MOE_GROUPED_MAX_DIM || g->K > MOE_GROUPED_MAX_DIM) return MOE_ERR_UNSUPPORTED;
-    if (int8) {
+    if (codes == Codes::kInt8) {
         // (int32 sums of products of at most 2^14: K < 2^17)
         if (g->K % 16 != 0 || g->N % 8 != 0 || g->K >= (1 << 17)) return MOE_ERR_UNSUPPORTED;
+    } else if (codes == Codes::kMxfp4) {
+        if (g->K % 32 != 0 || g->N % 8 != 0) return MOE_ERR_UNSUPPORTED;
     } else {
         const int words = g->dtype == MOE_DTYPE_BF16 ? 8 : 4;
         if (g->K % words != 0 || g->N % words != 0) return MOE_ERR_UNSUPPORTED;
     }
     if (grouped_tiles(*g) >= (1 << 24) - 8 * MOE_MAX_EXPERTS) return MOE_ERR_UNSUPPORTED;
-    if (!int8 && ceil_div(static_cast<int64_t>(g->E) * g->N * g->K, 1024) > kMaxLaunchItems / 256) return MOE_ERR_UNSUPPORTED;
+    if (codes == Codes::kNone && ceil_div(static_cast<int64_t>(g->E) * g->N * g->K, 1024) > kMaxLaunchItems / 256) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
+}
+
+// Routing by scores.  `router`: the logits come from x and w_router.
+moe_status_t check_gating(const moe_gating_t* g, bool router) {
+    if (g == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+    if (g->T < 0 || g->E < 1 || g->k < 1 || g->k > g->E) return MOE_ERR_INVALID_ARGUMENT;
+    if (g->score != MOE_SCORE_SOFTMAX && g->score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARGUMENT;
+    if (g->groups < 1 || g->groups_kept < 1 || g->groups_kept > g->groups || g->E % g->groups != 0)
+        return MOE_ERR_INVALID_ARGUMENT;
+    if (g->group_top != 1 && g->group_top != 2) return MOE_ERR_INVALID_ARGUMENT;
+    if (static_cast<int64_t>(g->groups_kept) * (g->E / g->groups) < g->k) return MOE_ERR_INVALID_ARGUMENT;
+    if (!std::isfinite(g->scale)) return MOE_ERR_INVALID_ARGUMENT;
+    if (g->E > MOE_MAX_EXPERTS || g->k > MOE_MAX_TOPK) return MOE_ERR_UNSUPPORTED;
+    // (a launch counts its work-items in 32 bits: at most 256 lanes per token)
+    if (g->T > INT32_MAX / g->k || g->T > kMaxLaunchItems / 256) return MOE_ERR_UNSUPPORTED;
+    if (router) {
+        if (g->d < 1 || (g->dtype != MOE_DTYPE_F32 && g->dtype != MOE_DTYPE_BF16)) return MOE_ERR_INVALID_ARGUMENT;
+        if (g->dtype == MOE_DTYPE_BF16 && g->d % 64 != 0) return MOE_ERR_UNSUPPORTED;
+    }
+    return MOE_OK;
+}
+
+size_t gating_ws(const moe_gating_t& g) { return static_cast<size_t>(route_scored_blocks(g)) * g.E * 4; }
+
+// Rows of 4-bit codes: whole blocks of 32, a workgroup per 2048 values.
+moe_status_t check_mxfp4_rows(int64_t rows, int32_t cols, int32_t dtype) {
+    if (rows < 0 || cols <= 0) return MOE_ERR_INVALID_ARGUMENT;
+    if (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARGUMENT;
+    if (cols % 32 != 0 || cols > MOE_GROUPED_MAX_DIM || rows > kMaxLaunchItems / 256) return MOE_ERR_UNSUPPORTED;
+    return rows * (cols / 8) > kMaxLaunchItems - 255 ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
 // The workspace of a weight gradient: required only when it needs one.
@@ -376,6 +412,83 @@ moe_status_t moe_combine(const moe_problem_t* p, const void* y_perm, const int32
     hipStream_t s = static_cast<hipStream_t>(stream);
     clear_hip_error();
     MOE_LAUNCH(launch_combine(*p, y_perm, assign_pos, topk_gates, y, s));
+    return MOE_OK;
+}
+
+moe_status_t moe_combine_backward(const moe_problem_t* p, const void* dy, const void* y_perm,
+                                  const int32_t* assign_pos, const float* topk_gates, void* dy_perm, float* dgates,
+                                  void* stream) {
+    MOE_TRY(check_problem(p));
+    if (p->T == 0) return MOE_OK;
+    if (dy_perm == nullptr && dgates == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+    MOE_TRY(need(dy));
+    MOE_TRY(optional(y_perm));
+    MOE_TRY(need(assign_pos));
+    MOE_TRY(need(topk_gates));
+    MOE_TRY(optional(dy_perm));
+    MOE_TRY(optional(dgates));
+    if (dgates != nullptr) MOE_TRY(need(y_perm));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    clear_hip_error();
+    MOE_LAUNCH(launch_combine_backward(*p, dy, y_perm, assign_pos, topk_gates, dy_perm, dgates, s));
+    return MOE_OK;
+}
+
+moe_status_t moe_route_scored_workspace_size(const moe_gating_t* g, size_t* bytes) {
+    if (bytes == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+    MOE_TRY(check_gating(g, false));
+    *bytes = gating_ws(*g);
+    return MOE_OK;
+}
+
+moe_status_t moe_route_scored(const moe_gating_t* g, const void* x, const void* w_router, const float* logits_in,
+                              float* logits_out, const float* bias, int32_t* topk_ids, float* topk_gates,
+                              float* score_sums, void* ws, size_t ws_bytes, void* stream) {
+    MOE_TRY(check_gating(g, logits_in == nullptr));
+    if (g->T > 0) {
+        if (logits_in != nullptr) {
+            MOE_TRY(need(logits_in));
+        } else {
+            MOE_TRY(need(x));
+            MOE_TRY(need(w_router));
+            MOE_TRY(need(logits_out));
+        }
+        MOE_TRY(need(topk_ids));
+        MOE_TRY(need(topk_gates));
+    }
+    MOE_TRY(optional(bias));
+    MOE_TRY(optional(score_sums));
+    if (score_sums != nullptr && gating_ws(*g) > 0) {
+        MOE_TRY(need(ws));
+        if (ws_bytes < gating_ws(*g)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    }
+    if (g->T == 0 && score_sums == nullptr) return MOE_OK;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    clear_hip_error();
+    const float* l = logits_in;
+    if (l == nullptr && g->T > 0) {
+        const moe_problem_t p{g->T, g->d, g->E, g->k, 64, g->dtype};
+        MOE_LAUNCH(launch_router_logits(p, x, w_router, logits_out, s));
+        l = logits_out;
+    }
+    MOE_LAUNCH(launch_route_scored(*g, l, bias, topk_ids, topk_gates, score_sums, static_cast<float*>(ws), s));
+    return MOE_OK;
+}
+
+moe_status_t moe_route_scored_backward(const moe_gating_t* g, const float* logits, const int32_t* topk_ids,
+                                       const float* dgates, const float* dscore_sums, int32_t dlogits_dtype,
+                                       void* dlogits, void* stream) {
+    MOE_TRY(check_gating(g, false));
+    if (dlogits_dtype != MOE_DTYPE_F32 && dlogits_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARGUMENT;
+    if (g->T == 0) return MOE_OK;
+    MOE_TRY(need(logits));
+    MOE_TRY(need(topk_ids));
+    MOE_TRY(need(dgates));
+    MOE_TRY(optional(dscore_sums));
+    MOE_TRY(need(dlogits));
+    clear_hip_error();
+    MOE_LAUNCH(launch_route_scored_backward(*g, logits, topk_ids, dgates, dscore_sums, dlogits_dtype, dlogits,
+                                            static_cast<hipStream_t>(stream)));
     return MOE_OK;
 }
 
@@ -621,14 +734,14 @@ moe_status_t moe_grouped_workspace_size(const moe_grouped_t* g, int32_t op, size
     if (bytes == nullptr) return MOE_ERR_INVALID_ARGUMENT;
     if (op != MOE_GROUPED_OP_MATMUL && op != MOE_GROUPED_OP_BACKWARD && op != MOE_GROUPED_OP_INT8)
         return MOE_ERR_INVALID_ARGUMENT;
-    MOE_TRY(check_grouped(g, op == MOE_GROUPED_OP_INT8));
+    MOE_TRY(check_grouped(g, op == MOE_GROUPED_OP_INT8 ? Codes::kInt8 : Codes::kNone));
     *bytes = grouped_ws_bytes(*g, op);
     return MOE_OK;
 }
 
 moe_status_t moe_grouped_matmul(const moe_grouped_t* g, const void* a, const void* w, const int32_t* offsets,
                                 void* c, void*, size_t, void* stream) {
-    MOE_TRY(check_grouped(g, false));
+    MOE_TRY(check_grouped(g, Codes::kNone));
     if (g->rows == 0) return MOE_OK;
     MOE_TRY(need(a));
     MOE_TRY(need(w));
@@ -642,7 +755,7 @@ moe_status_t moe_grouped_matmul(const moe_grouped_t* g, const void* a, const voi
 moe_status_t moe_grouped_matmul_backward(const moe_grouped_t* g, const void* a, const void* w,
                                          const int32_t* offsets, const void* dc, void* da, void* dw, void* ws,
                                          size_t ws_bytes, void* stream) {
-    MOE_TRY(check_grouped(g, false));
+    MOE_TRY(check_grouped(g, Codes::kNone));
     if (da == nullptr && dw == nullptr && g->rows > 0) return MOE_ERR_INVALID_ARGUMENT;
     MOE_TRY(need(offsets));
     MOE_TRY(optional(da));
@@ -676,7 +789,7 @@ moe_status_t moe_quantize_rows_int8(const void* src, int64_t rows, int32_t cols,
 moe_status_t moe_grouped_matmul_int8(const moe_grouped_t* g, const void* a, const float* a_scales, const void* w,
                                      const float* w_scales, const int32_t* offsets, void* c, void*, size_t,
                                      void* stream) {
-    MOE_TRY(check_grouped(g, true));
+    MOE_TRY(check_grouped(g, Codes::kInt8));
     if (offsets == nullptr && g->E != 1) return MOE_ERR_INVALID_ARGUMENT;
     if (g->rows == 0) return MOE_OK;
     MOE_TRY(need(a));
@@ -687,6 +800,46 @@ moe_status_t moe_grouped_matmul_int8(const moe_grouped_t* g, const void* a, cons
     MOE_TRY(need(c));
     clear_hip_error();
     MOE_LAUNCH(launch_grouped_int8(*g, a, a_scales, w, w_scales, offsets, c, static_cast<hipStream_t>(stream)));
+    return MOE_OK;
+}
+
+moe_status_t moe_quantize_rows_mxfp4(const void* src, int64_t rows, int32_t cols, int32_t dtype, void* codes,
+                                     void* scales, void* stream) {
+    MOE_TRY(check_mxfp4_rows(rows, cols, dtype));
+    if (rows == 0) return MOE_OK;
+    MOE_TRY(need(src));
+    MOE_TRY(need(codes));
+    MOE_TRY(need(scales));
+    clear_hip_error();
+    MOE_LAUNCH(launch_quant_rows_mxfp4(src, rows, cols, dtype, codes, scales, static_cast<hipStream_t>(stream)));
+    return MOE_OK;
+}
+
+moe_status_t moe_dequantize_rows_mxfp4(const void* codes, const void* scales, int64_t rows, int32_t cols,
+                                       int32_t dtype, void* dst, void* stream) {
+    MOE_TRY(check_mxfp4_rows(rows, cols, dtype));
+    if (rows == 0) return MOE_OK;
+    MOE_TRY(need(codes));
+    MOE_TRY(need(scales));
+    MOE_TRY(need(dst));
+    clear_hip_error();
+    MOE_LAUNCH(launch_dequant_rows_mxfp4(codes, scales, rows, cols, dtype, dst, static_cast<hipStream_t>(stream)));
+    return MOE_OK;
+}
+
+moe_status_t moe_grouped_matmul_mxfp4(const moe_grouped_t* g, const void* a, const void* a_scales, const void* w,
+                                      const void* w_scales, const int32_t* offsets, void* c, void* stream) {
+    MOE_TRY(check_grouped(g, Codes::kMxfp4));
+    if (offsets == nullptr && g->E != 1) return MOE_ERR_INVALID_ARGUMENT;
+    if (g->rows == 0) return MOE_OK;
+    MOE_TRY(need(a));
+    MOE_TRY(need(a_scales));
+    MOE_TRY(need(w));
+    MOE_TRY(need(w_scales));
+    MOE_TRY(optional(offsets));
+    MOE_TRY(need(c));
+    clear_hip_error();
+    MOE_LAUNCH(launch_grouped_mxfp4(*g, a, a_scales, w, w_scales, offsets, c, static_cast<hipStream_t>(stream)));
     return MOE_OK;
 }
 

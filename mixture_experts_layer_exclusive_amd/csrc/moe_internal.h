@@ -93,6 +93,22 @@ hipError_t launch_expert_ffn(const moe_problem_t& p, const void* x_perm, const v
 hipError_t launch_combine(const moe_problem_t& p, const void* y_perm, const int32_t* assign_pos,
                           const float* gates, void* y, hipStream_t s);
 
+// Its gradient (dy_perm, or dgates with y_perm, may be NULL).
+hipError_t launch_combine_backward(const moe_problem_t& p, const void* dy, const void* y_perm,
+                                   const int32_t* assign_pos, const float* gates, void* dy_perm, float* dgates,
+                                   hipStream_t s);
+
+// ---- routing by scores -------------------------------------------------------
+
+// Workgroups of the forward; each leaves E partial score sums.
+int64_t route_scored_blocks(const moe_gating_t& g);
+// (score_sums and partial: both or neither)
+hipError_t launch_route_scored(const moe_gating_t& g, const float* logits, const float* bias, int32_t* ids,
+                               float* gates, float* score_sums, float* partial, hipStream_t s);
+hipError_t launch_route_scored_backward(const moe_gating_t& g, const float* logits, const int32_t* ids,
+                                        const float* dgates, const float* dscore_sums, int dtype, void* dlogits,
+                                        hipStream_t s);
+
 // ---- backward (bf16) ------------------------------------------------------
 
 // Padded per-expert column count of the weight-gradient operands: every
@@ -173,5 +189,14 @@ hipError_t launch_grouped_int8(const moe_grouped_t& g, const void* a, const floa
                                const float* w_scales, const int32_t* offsets, void* c, hipStream_t s);
 hipError_t launch_quant_rows_int8(const void* src, int64_t rows, int cols, int dtype, void* codes, float* scales,
                                   hipStream_t s);
+
+// ---- 4-bit microscaled floats -----------------------------------------------
+
+hipError_t launch_quant_rows_mxfp4(const void* src, int64_t rows, int cols, int dtype, void* codes, void* scales,
+                                   hipStream_t s);
+hipError_t launch_dequant_rows_mxfp4(const void* codes, const void* scales, int64_t rows, int cols, int dtype,
+                                     void* dst, hipStream_t s);
+hipError_t launch_grouped_mxfp4(const moe_grouped_t& g, const void* a, const void* sa, const void* w, const void* sw,
+                                const int32_t* offsets, void* c, hipStream_t s);
 
 }  // namespace moe
