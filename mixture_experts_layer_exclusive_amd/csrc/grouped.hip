@@ -57,16 +57,6 @@ __global__ __launch_bounds__(256) void grouped_parts_kernel(const float* __restr
 
 // ---- the launches ---------------------------------------------------------------------
 
-// CUs of the device of stream s.
-int compute_units(hipStream_t s) {
-    hipDevice_t dev = 0;
-    int cus = 0;
-    if (hipStreamGetDevice(s, &dev) != hipSuccess ||
-        hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
-        return kCus;
-    return cus;
-}
-
 struct Args {
     const moe_grouped_t& g;
     const void* X;

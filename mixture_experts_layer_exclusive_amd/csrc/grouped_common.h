@@ -20,6 +20,9 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x16_t __attribute__((ext_vector_type(16)));
 
 constexpr int kBf16 = 0, kF32 = 1, kI8 = 2;
+// 4-bit microscaled floats.  To the loads and the layout in LDS they are bytes, as
+// kI8: what the kernels call K is a row's length in bytes, half its values.
+constexpr int kMx4 = 3;
 
 // ---- queues and the tile order ---------------------------------------------
 
@@ -299,6 +302,33 @@ __device__ __forceinline__ void lds_dma16_b(uint64_t base, uint32_t voff, uint32
         : "memory");
 }
 
+// 4 or 16 bytes per lane (consecutive lanes', consecutive in LDS from lds_base) of
+// the `bytes` bytes from base, as above.  Each 4 bytes are checked by themselves:
+// beyond the end they are zeros.  base and bytes are multiples of 4.
+template <int WIDTH>
+__device__ __forceinline__ void lds_dma_bounded(uint64_t base, uint32_t bytes, uint32_t voff, uint32_t lds_base) {
+    static_assert(WIDTH == 4 || WIDTH == 16, "a load's bytes per lane");
+    i32x4_t rsrc;
+    rsrc[0] = static_cast<int>(static_cast<uint32_t>(base));
+    rsrc[1] = static_cast<int>(static_cast<uint32_t>(base >> 32) & 0xffffu);
+    rsrc[2] = static_cast<int>(bytes);
+    rsrc[3] = static_cast<int>(kRsrcWord3);
+    if constexpr (WIDTH == 16)
+        asm volatile(
+            "s_nop 4\n\t"
+            "buffer_load_dwordx4 %0, %1, 0 offen lds"
+            :
+            : "v"(voff), "s"(rsrc), "{m0}"(lds_base)
+            : "memory");
+    else
+        asm volatile(
+            "s_nop 4\n\t"
+            "buffer_load_dword %0, %1, 0 offen lds"
+            :
+            : "v"(voff), "s"(rsrc), "{m0}"(lds_base)
+            : "memory");
+}
+
 __device__ __forceinline__ uint64_t uniform64(uint64_t v) {
     const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
     const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
@@ -307,7 +337,7 @@ __device__ __forceinline__ uint64_t uniform64(uint64_t v) {
 
 // ---- a slice of an operand in LDS ------------------------------------------------
 //
-// A slice is 128 bytes of q (64 bf16, 32 f32 or 128 int8 values) of TX tile
+// A slice is 128 bytes of q (64 bf16, 32 f32, 128 int8 or 256 4-bit values) of TX tile
 // rows, TX * 128 bytes in all.
 //   row-major     an LDS row is one tile row's 128 bytes of q: 8 words of 16
 //                 bytes, word c at place c ^ ((row >> 1) & 7), which spreads the
@@ -417,10 +447,50 @@ __device__ __forceinline__ void multiply(const i32x4_t& y, const i32x4_t& x, Acc
                                                       acc, 0, 0, 0);
     } else if constexpr (TY == kI8) {
         acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(y, x, acc, 0, 0, 0);
-    } else {
+    } else if constexpr (TY == kF32) {
         const f32x4_t yf = __builtin_bit_cast(f32x4_t, y), xf = __builtin_bit_cast(f32x4_t, x);
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(yf[i], xf[i], acc, 0, 0, 0);
+    }
+}
+
+// ---- scales of 4-bit values ------------------------------------------------------
+//
+// A step's 16 bytes per half wave are one block of 32 values (step kk: block 2 kk +
+// half of the slice), and the MFMA takes the block's scale byte from byte kk of a
+// register.  A slice has 8 scale bytes per row, which lie as the rows do in
+// [ceil(K / 256)][rows][8]; in LDS X's rows come first, then Y's, 8 bytes each.  They
+// are loaded up to the tile's last byte and no further (the rows start and end at any
+// multiple of 8).
+
+// Which of a row's 8 scale bytes belong to this half wave's steps 0 .. 3, as
+// v_perm selectors; blocks from `valid` on get the scale byte 0 (their codes are
+// zeros, but a byte of 255, NaN, would count).
+__device__ __forceinline__ uint32_t scale_select(int half, int valid) {
+    uint32_t sel = 0;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) sel |= (2 * kk + half < valid ? 2u * kk + half : 0x0cu) << (8 * kk);
+    return sel;
+}
+
+__device__ __forceinline__ int pick_scales(const uint2& raw, uint32_t sel) {
+    return static_cast<int>(__builtin_amdgcn_perm(raw.y, raw.x, sel));
+}
+
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+
+// multiply of step kk: sy and sx hold the four steps' scales.  (A 4-bit operand
+// is half of the instruction's widest; the other half is not read.)
+__device__ __forceinline__ void multiply_mx4(int kk, const i32x4_t& y, const i32x4_t& x, int sy, int sx, f32x16_t& acc) {
+    const i32x8_t y8 = __builtin_shufflevector(y, y, 0, 1, 2, 3, -1, -1, -1, -1);
+    const i32x8_t x8 = __builtin_shufflevector(x, x, 0, 1, 2, 3, -1, -1, -1, -1);
+    constexpr int kE2m1 = 4;
+    // (the byte is part of the instruction)
+    switch (kk) {
+        case 0: acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(y8, x8, acc, kE2m1, kE2m1, 0, sy, 0, sx); break;
+        case 1: acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(y8, x8, acc, kE2m1, kE2m1, 1, sy, 1, sx); break;
+        case 2: acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(y8, x8, acc, kE2m1, kE2m1, 2, sy, 2, sx); break;
+        default: acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(y8, x8, acc, kE2m1, kE2m1, 3, sy, 3, sx); break;
     }
 }
 

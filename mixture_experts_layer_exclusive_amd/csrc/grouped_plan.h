@@ -70,11 +70,8 @@ struct Plan {
 
 // The cheapest variant for mode `mode` of problem g.  The host knows the queues'
 // number and sum only: a queue is taken to end in half a tile.
-Plan plan_for(const moe_grouped_t& g, int mode, bool int8) {
-    const bool f32 = g.dtype == MOE_DTYPE_F32 && !int8;
-    const Cost* const cost = mode == kTN ? (f32 ? kCostW32 : kCostW16) : (f32 ? kCost32 : kCost16);
+Plan plan_of(const moe_grouped_t& g, int mode, bool f32, const Cost* cost, int64_t qs) {
     const int64_t M = g.N, P = mode == kNT ? g.N : g.K;
-    const int64_t qs = int8 ? 128 : (f32 ? 32 : 64);
     const int64_t live = std::max<int64_t>(std::min<int64_t>(g.E, g.rows), 1);
     Plan best{kTile128, 1, 0};
     double least = 0;
@@ -132,6 +129,15 @@ Plan plan_for(const moe_grouped_t& g, int mode, bool int8) {
     }
     return best;
 }
+
+Plan plan_for(const moe_grouped_t& g, int mode, bool int8) {
+    const bool f32 = g.dtype == MOE_DTYPE_F32 && !int8;
+    const Cost* const cost = mode == kTN ? (f32 ? kCostW32 : kCostW16) : (f32 ? kCost32 : kCost16);
+    return plan_of(g, mode, f32, cost, int8 ? 128 : (f32 ? 32 : 64));
+}
+
+// The forward of 4-bit floats.
+Plan plan_mxfp4(const moe_grouped_t& g) { return plan_of(g, kNT, false, kCost16, 256); }
 
 size_t parts_bytes(const moe_grouped_t& g, const Plan& p) {
     return p.parts > 1 ? static_cast<size_t>(p.parts) * g.E * g.N * g.K * 4 : 0;

@@ -43,9 +43,14 @@ namespace {
 // 1045 us), of zeros 2.4 GHz (786 us), and this kernel 1.5 GHz.  One queue of
 // those rows takes 1358 us; 1334 over operands from the caches only, 1332
 // without half of the fragment reads.  8 queues of 2048: 1428, 1328, 1406.
-template <int MB, int NB, int NS, typename O>
+template <int MB, int NB, int NS, typename O, bool MX = false>
 struct TileLds {
-    static constexpr int STAGE = 64 * (MB + NB) * 128;
+    static constexpr int OPERANDS = 64 * (MB + NB) * 128;
+    // (4-bit values) loads of scales per wave and slice, 16 bytes per lane where they
+    // fill one load of each wave, else 4, and the bytes of one
+    static constexpr int SW = MB + NB >= 8 ? 16 : 4;
+    static constexpr int SL = MX ? (512 * (MB + NB) + 4 * 64 * SW - 1) / (4 * 64 * SW) : 0;
+    static constexpr int STAGE = OPERANDS + SL * 4 * 64 * SW;
     static constexpr int NP = sizeof(O) == 2 && NB >= 2 ? 2 : 1;  // column blocks the epilogue stages at a time
     static constexpr int EROW = NP * 32 * sizeof(O);  // bytes of a staged row: a 128-byte line (bf16, NB = 1: 64)
     static constexpr int EPI = 32 * EROW;             // staged bytes per wave
@@ -65,21 +70,24 @@ struct TileLds {
 template <int TY, int MODE, int MB, int NB, int NS, typename O>
 __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block, int blocks, const void* __restrict__ Xp,
                                              const void* __restrict__ Yp, const int32_t* __restrict__ offsets, int E,
-                                             int rows, int N, int K, O* __restrict__ C, const float* __restrict__ sx,
-                                             const float* __restrict__ sy, int parts) {
-    using Lds = TileLds<MB, NB, NS, O>;
+                                             int rows, int N, int K, O* __restrict__ C, const void* __restrict__ sx,
+                                             const void* __restrict__ sy, int parts) {
+    constexpr bool MX = TY == kMx4;
+    using Lds = TileLds<MB, NB, NS, O, MX>;
     constexpr bool XC = MODE == kTN;             // X column-major
     constexpr bool YC = MODE != kNT;             // Y column-major
-    static_assert(TY != kI8 || MODE == kNT, "int8: forward only");
+    static_assert((TY != kI8 && TY != kMx4) || MODE == kNT, "codes: forward only");
     constexpr int TM = 64 * MB, TN = 64 * NB;    // output tile
     using XS = Slice<TY, XC, TM>;
     using YS = Slice<TY, YC, TN>;
     constexpr int EB = XS::EB;
     constexpr int QS = 128 / EB;                 // q per slice
     constexpr int XL = XS::LOADS / 4, YL = YS::LOADS / 4;  // loads per wave and slice
-    constexpr int NL = XL + YL;
+    constexpr int SL = Lds::SL;
+    constexpr int NL = XL + YL + SL;
     constexpr int X_BYTES = TM * 128;
     constexpr int STAGE = Lds::STAGE;
+    constexpr int SC_AT = Lds::OPERANDS;         // the scales within a stage
     constexpr int NM = MB * NB;
     constexpr int NR = MB + NB;
     constexpr bool BF_OUT = sizeof(O) == 2;
@@ -161,6 +169,14 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
     // This wave's loads j fill the KB at (wave * L + j) * 1024 of the operand's
     // part of the stage.  Bit j of the tail masks: the lane's part of load j is
     // out of range in the tile's last slice.
+    // (4-bit values) A wave's loads of scales are all X's or all Y's: the SL from
+    // wave * SL on, of X's scales and then Y's.
+    constexpr int SC_LOAD = 64 * Lds::SW, SC_X = 512 * MB;
+    const bool sc_y = wave * SL * SC_LOAD >= SC_X;
+    const uint32_t sc_off = wave * SL * SC_LOAD - (sc_y ? SC_X : 0) + lane * Lds::SW;
+    uint64_t sc_base = 0;
+    uint32_t sc_bytes = 0;                       // of the tile's rows
+    static_assert(!MX || SC_X % (SL * SC_LOAD) == 0, "a wave's scales are of one operand");
     uint32_t xoff[XL], yoff[YL], xtail = 0, ytail = 0;
     bool tailed = false;                         // the last slice is not a whole one
     auto aim = [&](const Tile& t) {
@@ -188,6 +204,12 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
         }
         xbase = uniform64(xbase);
         ybase = uniform64(ybase);
+        if constexpr (MX) {
+            const char* const from = static_cast<const char*>(sc_y ? sy : sx);
+            const int64_t row = sc_y ? static_cast<int64_t>(t.e) * N + t.p0 : t.m0;
+            sc_base = uniform64(reinterpret_cast<uint64_t>(from + row * 8));
+            sc_bytes = __builtin_amdgcn_readfirstlane(8 * (sc_y ? min(TN, P - t.p0) : t.m1 - t.m0));
+        }
     };
     auto nothing = [&]() {
         left = 0x7fffffff;
@@ -196,6 +218,7 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
         for (int j = 0; j < XL; ++j) xoff[j] = kOutOfRange;
 #pragma unroll
         for (int j = 0; j < YL; ++j) yoff[j] = kOutOfRange;
+        sc_bytes = 0;
     };
     // the tiles between the load side and the multiplying side (at most two, of
     // one slice each, and the one being multiplied), kept by each wave for itself
@@ -224,6 +247,11 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
     };
     // load l (< NL) of the next slice to load, into stage `so`
     auto dma = [&](int l, uint32_t so) {
+        if (l < SL) {
+            lds_dma_bounded<Lds::SW>(sc_base, sc_bytes, sc_off + l * SC_LOAD, lds0 + so + SC_AT + (wave * SL + l) * SC_LOAD);
+            return;
+        }
+        l -= SL;
         const bool y = l < YL;
         const int j = y ? l : l - YL;
         lds_dma16_b(y ? ybase : xbase, y ? yoff[j < YL ? j : 0] : xoff[j < XL ? j : 0],
@@ -241,6 +269,7 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
     auto loaded = [&]() {
         xbase += xstep;
         ybase += ystep;
+        if constexpr (MX) sc_base += 8 * (sc_y ? static_cast<int64_t>(E) * N : static_cast<int64_t>(rows));
         if (--left == 0) {
             if (STREAM) next_load();
             else nothing();
@@ -254,6 +283,18 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
     auto read_frag = [&](int kk, int i, uint32_t so) {
         f[kk][i] = i < MB ? xfrag.read(smem, so, i, kk) : yfrag.read(smem + X_BYTES, so, i - MB, kk);
     };
+    // (4-bit values) the scales of the slice being multiplied, and, as they lie in
+    // LDS, of the next one: X blocks, then Y blocks
+    int scale[MX ? NR : 1];
+    uint2 next_scale[MX ? NR : 1];
+    const uint32_t sc_whole = MX ? scale_select(lane >> 5, 8) : 0;
+    const uint32_t sc_last = MX ? scale_select(lane >> 5, (K / 16 - 1) % 8 + 1) : 0;
+    const uint32_t sc_at = SC_AT + wm * MB * 256 + (lane & 31) * 8;
+    const uint32_t sc_at_y = SC_AT + TM * 8 + wn * NB * 256 + (lane & 31) * 8;
+    auto read_scale = [&](int i, uint32_t so) {
+        if constexpr (MX)
+            next_scale[i] = *reinterpret_cast<const uint2*>(smem + so + (i < MB ? sc_at + i * 256 : sc_at_y + (i - MB) * 256));
+    };
     Acc<TY> acc[NB][MB];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
@@ -262,7 +303,8 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
     // (there and back over X, so that two products in a row share a fragment: 1 %)
     auto mul = [&](int kk, int q) {
         const int mb = q / MB % 2 ? MB - 1 - q % MB : q % MB;
-        multiply<TY>(f[kk][MB + q / MB], f[kk][mb], acc[q / MB][mb]);
+        if constexpr (MX) multiply_mx4(kk, f[kk][MB + q / MB], f[kk][mb], scale[MB + q / MB], scale[mb], acc[q / MB][mb]);
+        else multiply<TY>(f[kk][MB + q / MB], f[kk][mb], acc[q / MB][mb]);
     };
 
     // the refilling loads go out over SLOTS MFMAs: those of step 1 after FREE,
@@ -278,7 +320,13 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
     constexpr int YOUNGER = (NS - 2) * NL + BEFORE3;
     static_assert((NS - 1) * NL < 64, "vmcnt");
     uint32_t so = 0;                             // the stage being multiplied
+    int n;                                       // slices of the tile still to multiply
     auto slice = [&]() {
+        if constexpr (MX) {
+            const uint32_t sel = n == 1 ? sc_last : sc_whole;
+#pragma unroll
+            for (int i = 0; i < NR; ++i) scale[i] = pick_scales(next_scale[i], sel);
+        }
         const uint32_t nso = so + STAGE == NS * STAGE ? 0 : so + STAGE;
         auto refill = [&](int p, uint32_t stage) {
 #pragma unroll
@@ -322,7 +370,10 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
             mul(3, q);
             refill(2 * NM - FREE + q, so);
 #pragma unroll
-            for (int i = q * NR / NM; i < (q + 1) * NR / NM; ++i) read_frag(0, i, nso);
+            for (int i = q * NR / NM; i < (q + 1) * NR / NM; ++i) {
+                read_frag(0, i, nso);
+                read_scale(i, nso);
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
         if (LATE == 0) loaded();
@@ -344,7 +395,7 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
         float rs[MB];
         if constexpr (TY == kI8) {
 #pragma unroll
-            for (int mb = 0; mb < MB; ++mb) rs[mb] = sx[min(mrow + mb * 32 + l32, t.m1 - 1)];
+            for (int mb = 0; mb < MB; ++mb) rs[mb] = static_cast<const float*>(sx)[min(mrow + mb * 32 + l32, t.m1 - 1)];
         }
         O* const out = C + (MODE == kTN ? static_cast<int64_t>(t.e) * N * K : 0) + static_cast<int64_t>(mrow) * P + pcol;
         f32x4_t cs[TY == kI8 ? NB : 1][4];
@@ -354,7 +405,7 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const int col = min(pcol + nb * 32 + 8 * g + 4 * half, P - 4);
-                    cs[nb][g] = *reinterpret_cast<const f32x4_t*>(sy + static_cast<int64_t>(t.e) * N + col);
+                    cs[nb][g] = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(sy) + static_cast<int64_t>(t.e) * N + col);
                 }
         }
 #pragma unroll
@@ -446,12 +497,15 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
     wait_vmcnt<(NS - 2) * NL + BEFORE0>();
     barrier_lds();
 #pragma unroll
-    for (int i = 0; i < NR; ++i) read_frag(0, i, 0);
+    for (int i = 0; i < NR; ++i) {
+        read_frag(0, i, 0);
+        read_scale(i, 0);
+    }
     __builtin_amdgcn_sched_barrier(0);
     // (one flat loop over slices, with the tile's end inside: nested loops make
     // the compiler move the accumulators between registers at every tile)
     Tile t;
-    int tiles = 0, n;
+    int tiles = 0;
     auto next_tile = [&]() {
         if (tiles == loading) return false;
         const int* const r = ring + (tiles & 3) * 8;
@@ -478,8 +532,8 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
 template <int TY, int MODE, int MB, int NB, int NS, typename O>
 __global__ __launch_bounds__(256, (MB * NB > 4 ? 1 : 2)) void grouped_tile_kernel(
     const void* __restrict__ Xp, const void* __restrict__ Yp, const int32_t* __restrict__ offsets, int E, int rows,
-    int N, int K, O* __restrict__ C, const float* __restrict__ sx, const float* __restrict__ sy, int parts) {
-    __shared__ __attribute__((aligned(1024))) char smem[TileLds<MB, NB, NS, O>::BYTES];
+    int N, int K, O* __restrict__ C, const void* __restrict__ sx, const void* __restrict__ sy, int parts) {
+    __shared__ __attribute__((aligned(1024))) char smem[TileLds<MB, NB, NS, O, TY == kMx4>::BYTES];
     grouped_tile<TY, MODE, MB, NB, NS, O>(smem, blockIdx.x, gridDim.x, Xp, Yp, offsets, E, rows, N, K, C, sx, sy, parts);
 }
 
@@ -496,15 +550,17 @@ __global__ __launch_bounds__(256, (MB * NB > 4 ? 1 : 2)) void grouped_tile_kerne
 // multiplied, then its stage takes the loads of the slice after next.  Slices
 // past the end are loaded out of range (zeros, no traffic), so that the number
 // of loads in flight, and with it the waits, is constant.
-constexpr int split_lds(int MB, int NB) { return 4 * 2 * (32 * MB + 32 * NB) * 128; }
+// (4-bit values: a slice's scales, 8 bytes per row, after its operands)
+constexpr int split_lds(int MB, int NB, bool MX = false) { return 4 * 2 * (32 * MB + 32 * NB) * (MX ? 136 : 128); }
 
 // smem: split_lds bytes, 1024-byte aligned
 template <int TY, int MODE, int MB, int NB, typename O>
 __device__ __forceinline__ void grouped_split(char* __restrict__ smem, int block, const void* __restrict__ Xp,
                                               const void* __restrict__ Yp, const int32_t* __restrict__ offsets, int E,
-                                              int rows, int N, int K, O* __restrict__ C, const float* __restrict__ sx,
-                                              const float* __restrict__ sy) {
-    static_assert(MODE != kTN && (TY != kI8 || MODE == kNT), "no weight gradients; int8: forward only");
+                                              int rows, int N, int K, O* __restrict__ C, const void* __restrict__ sx,
+                                              const void* __restrict__ sy) {
+    constexpr bool MX = TY == kMx4;
+    static_assert(MODE != kTN && ((TY != kI8 && !MX) || MODE == kNT), "no weight gradients; codes: forward only");
     constexpr bool YC = MODE != kNT;
     constexpr int TM = 32 * MB, TN = 32 * NB;
     using XS = Slice<TY, false, TM>;
@@ -512,13 +568,14 @@ __device__ __forceinline__ void grouped_split(char* __restrict__ smem, int block
     constexpr int EB = XS::EB;
     constexpr int QS = 128 / EB;
     constexpr int X_BYTES = TM * 128;
-    constexpr int STAGE = (TM + TN) * 128;
+    constexpr int SC_AT = (TM + TN) * 128;       // the scales within a stage
+    constexpr int STAGE = SC_AT + (MX ? (TM + TN) * 8 : 0);
     constexpr int RING = 2 * STAGE;              // per wave
     constexpr int PADC = TN + 4;                 // row length of a partial tile in LDS
     static_assert(TM * PADC * 4 <= RING && sizeof(Queues) <= 4 * RING, "LDS");
     using Val = std::conditional_t<TY == kI8, int, float>;
     typedef Val val4_t __attribute__((ext_vector_type(4)));
-    static_assert(4 * RING == split_lds(MB, NB), "LDS");
+    static_assert(4 * RING == split_lds(MB, NB, MX), "LDS");
     Queues& queues = *reinterpret_cast<Queues*>(smem);
 
     const int P = MODE == kNT ? N : K;
@@ -555,6 +612,13 @@ __device__ __forceinline__ void grouped_split(char* __restrict__ smem, int block
         yoff[j] = YS::offset(j, lane, static_cast<uint32_t>(yrow), P - t.p0);
         ytail |= (YS::beyond(j, lane, qtail) ? 1u : 0u) << j;
     }
+    // (4-bit values) the scales of the tile's rows
+    const uint64_t sx0 = MX ? uniform64(reinterpret_cast<uint64_t>(sx) + static_cast<uint64_t>(t.m0) * 8) : 0;
+    const uint64_t sy0 =
+        MX ? uniform64(reinterpret_cast<uint64_t>(sy) + static_cast<uint64_t>(static_cast<int64_t>(t.e) * N + t.p0) * 8) : 0;
+    const uint32_t sx_bytes = 8 * (t.m1 - t.m0), sy_bytes = 8 * min(TN, P - t.p0);
+    const uint32_t sc_whole = MX ? scale_select(lane >> 5, 8) : 0;
+    const uint32_t sc_last = MX ? scale_select(lane >> 5, (K / 16 - 1) % 8 + 1) : 0;
     const Fragments<TY, false, TM, MB> xfrag(lane, 0);
     const Fragments<TY, YC, TN, NB> yfrag(lane, 0);
     Acc<TY> acc[NB][MB];
@@ -567,7 +631,7 @@ __device__ __forceinline__ void grouped_split(char* __restrict__ smem, int block
     // what was there, and only rows of C that are not stored see it)
     auto stream = [&](auto nx_c) {
         constexpr int NX = decltype(nx_c)::value;
-        constexpr int NL = YS::LOADS + NX;
+        constexpr int NL = YS::LOADS + NX + (MX ? MB + NB : 0);
         auto dma = [&](int kt, uint32_t st) {
             // all lanes out of range past the end, in the last slice those beyond it
             const uint32_t xo = kt >= nk ? ~0u : (kt == nk - 1 ? xtail : 0u);
@@ -578,9 +642,27 @@ __device__ __forceinline__ void grouped_split(char* __restrict__ smem, int block
 #pragma unroll
             for (int j = 0; j < NX; ++j)
                 lds_dma16_b(xbase + kt * xstep, xoff[j] | ((xo << (31 - j)) & kOutOfRange), lds_w + st + j * 1024);
+            if constexpr (MX) {
+#pragma unroll
+                for (int j = 0; j < MB; ++j)
+                    lds_dma_bounded<4>(sx0 + static_cast<uint64_t>(kt) * 8 * rows, kt < nk ? sx_bytes : 0, j * 256 + lane * 4,
+                               lds_w + st + SC_AT + j * 256);
+#pragma unroll
+                for (int j = 0; j < NB; ++j)
+                    lds_dma_bounded<4>(sy0 + static_cast<uint64_t>(kt) * 8 * E * N, kt < nk ? sy_bytes : 0, j * 256 + lane * 4,
+                               lds_w + st + SC_AT + (MB + j) * 256);
+            }
         };
         i32x4_t f[2][4][MB + NB];
-        auto read = [&](int b, uint32_t st) {
+        int scale[2][MX ? MB + NB : 1];
+        // (kt: the slice that lies there)
+        auto read = [&](int b, uint32_t st, int kt) {
+            if constexpr (MX) {
+                const uint32_t sel = kt == nk - 1 ? sc_last : sc_whole;
+#pragma unroll
+                for (int i = 0; i < MB + NB; ++i)
+                    scale[b][i] = pick_scales(*reinterpret_cast<const uint2*>(mine + st + SC_AT + i * 256 + (lane & 31) * 8), sel);
+            }
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
 #pragma unroll
@@ -595,7 +677,7 @@ __device__ __forceinline__ void grouped_split(char* __restrict__ smem, int block
         // behind each wait because of the empty statement)
         wait_vmcnt<NL>();
         asm volatile("" ::: "memory");
-        read(0, 0);
+        read(0, 0, wave);
         wait_vmcnt_lgkm0<63>();
         __builtin_amdgcn_sched_barrier(0);
         dma(wave + 8, 0);
@@ -606,13 +688,18 @@ __device__ __forceinline__ void grouped_split(char* __restrict__ smem, int block
                 const uint32_t st = u == 0 ? STAGE : 0;  // the stage of the slice after this one
                 wait_vmcnt<NL>();
                 asm volatile("" ::: "memory");
-                read(1 - u, st);
+                read(1 - u, st, kt + 4 * u + 4);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                        for (int mb = 0; mb < MB; ++mb) multiply<TY>(f[u][kk][MB + nb], f[u][kk][mb], acc[nb][mb]);
+                        for (int mb = 0; mb < MB; ++mb) {
+                            if constexpr (MX)
+                                multiply_mx4(kk, f[u][kk][MB + nb], f[u][kk][mb], scale[u][MB + nb], scale[u][mb], acc[nb][mb]);
+                            else
+                                multiply<TY>(f[u][kk][MB + nb], f[u][kk][mb], acc[nb][mb]);
+                        }
                 wait_vmcnt_lgkm0<63>();
                 __builtin_amdgcn_sched_barrier(0);
                 dma(kt + 4 * u + 12, st);
@@ -656,8 +743,8 @@ __device__ __forceinline__ void grouped_split(char* __restrict__ smem, int block
         for (int w = 1; w < 4; ++w) v += *reinterpret_cast<const val4_t*>(src + w * RING);
         f32x4_t o;
         if constexpr (TY == kI8) {
-            const float rs = sx[m];
-            const f32x4_t cs = *reinterpret_cast<const f32x4_t*>(sy + static_cast<int64_t>(t.e) * N + col);
+            const float rs = static_cast<const float*>(sx)[m];
+            const f32x4_t cs = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(sy) + static_cast<int64_t>(t.e) * N + col);
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] = static_cast<float>(v[i]) * rs * cs[i];
         } else {
@@ -672,9 +759,21 @@ __device__ __forceinline__ void grouped_split(char* __restrict__ smem, int block
 template <int TY, int MODE, int MB, int NB, typename O>
 __global__ __launch_bounds__(256) void grouped_split_kernel(
     const void* __restrict__ Xp, const void* __restrict__ Yp, const int32_t* __restrict__ offsets, int E, int rows,
-    int N, int K, O* __restrict__ C, const float* __restrict__ sx, const float* __restrict__ sy) {
-    __shared__ __attribute__((aligned(1024))) char smem[split_lds(MB, NB)];
+    int N, int K, O* __restrict__ C, const void* __restrict__ sx, const void* __restrict__ sy) {
+    __shared__ __attribute__((aligned(1024))) char smem[split_lds(MB, NB, TY == kMx4)];
     grouped_split<TY, MODE, MB, NB, O>(smem, blockIdx.x, Xp, Yp, offsets, E, rows, N, K, C, sx, sy);
+}
+
+// ---- the launches -----------------------------------------------------------------------
+
+// CUs of the device of stream s.
+int compute_units(hipStream_t s) {
+    hipDevice_t dev = 0;
+    int cus = 0;
+    if (hipStreamGetDevice(s, &dev) != hipSuccess ||
+        hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
+        return kCus;
+    return cus;
 }
 
 }  // namespace
