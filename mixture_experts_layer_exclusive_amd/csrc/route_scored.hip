@@ -6,11 +6,17 @@
 //   ids      the k largest c of the groups that stay, ties to the lower expert
 //   gates    scale * s of the chosen, over the sum of the chosen s if renormalised
 //
-// c decides between experts, so it is computed in 64 bits: two scores that
-// differ in the 30th bit are in the right order.  Without a bias c has the order
-// of the logits, which then stand for it (unless groups are valued by sums).
-#include <limits.h>
+// c decides between experts, so it is defined in 64 bits: two scores that differ in
+// the 30th bit are in the right order.  Without a bias c has the order of the
+// logits, which then stand for it (unless groups are valued by sums).
+//
+// For k <= 8 the choice is made in 32 bits by G lanes per token, and where it hangs
+// on a difference that 32 bits may have got wrong (about one token in 300), the whole
+// wave makes that token's choice again in 64 bits.
+#include <float.h>
 #include <math.h>
+
+#include <algorithm>
 
 #include "device_util.h"
 #include "moe_internal.h"
@@ -19,13 +25,8 @@ namespace moe {
 
 namespace {
 
-constexpr int kEpl = MOE_MAX_EXPERTS / 64;  // experts per lane: lane, lane + 64, ..
+constexpr int kEpl = MOE_MAX_EXPERTS / 64;  // experts per lane of a whole wave: lane, lane + 64, ..
 
-__device__ __forceinline__ double wave_max(double v) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v = fmax(v, __shfl_xor(v, off, 64));
-    return v;
-}
 template <typename T>
 __device__ __forceinline__ T wave_sum(T v) {
 #pragma unroll
@@ -36,264 +37,845 @@ __device__ __forceinline__ T wave_sum(T v) {
 // Whether (v, e) is chosen before (w, f).
 __device__ __forceinline__ bool before(double v, int e, double w, int f) { return v > w || (v == w && e < f); }
 
-// One wave per token, kTokens tokens per wave one after the other.
-constexpr int kTokens = 8;
+// LDS that a wave writes and reads by itself, in the order of the source (also where
+// the types differ).
+__device__ __forceinline__ void wave_lds() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+}
 
-__global__ __launch_bounds__(256) void route_scored_kernel(moe_gating_t g, const float* __restrict__ logits,
-                                                          const float* __restrict__ bias, int32_t* __restrict__ ids,
-                                                          float* __restrict__ gates, float* __restrict__ partial) {
-    __shared__ double s_c[4][MOE_MAX_EXPERTS];
-    __shared__ double s_v[4][MOE_MAX_EXPERTS];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// ---- values that carry their index ------------------------------------------------
+//
+// A key is a 64-bit float: a 32-bit c, with the index in the low bits such that of equal
+// c the lower index is the larger key (below zero a larger fraction is a smaller
+// number).  Then the larger of two keys is one instruction, index and all.
+
+__device__ __forceinline__ double key_max(double a, double b) {
+    double d;  // (fmax would quiet signalling NaNs first: there are none)
+    asm("v_max_f64 %0, %1, %2" : "=v"(d) : "v"(a), "v"(b));
+    return d;
+}
+__device__ __forceinline__ double key_min(double a, double b) {
+    double d;
+    asm("v_min_f64 %0, %1, %2" : "=v"(d) : "v"(a), "v"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t key_low(bool negative, int e) { return static_cast<uint32_t>(negative ? e : 255 - e); }
+__device__ __forceinline__ int key_index(double key) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, key);
+    const int low = static_cast<int>(b & 255u);
+    return b >> 63 ? low : 255 - low;
+}
+
+// An expert that is out: below every c.
+__device__ __forceinline__ double out_key(int e) {
+    return __builtin_bit_cast(double, 0xffefffff00000000ull | static_cast<uint32_t>(e));
+}
+
+// c in 32 bits: its bits are the upper half.  (Any float's are those of a finite
+// 64-bit one, minus infinity's of one above out_key.)
+__device__ __forceinline__ double key32(float c, int e) {
+    c = c == c ? c + 0.f : -INFINITY;  // (a NaN comes last; -0 is 0)
+    const uint32_t hi = __float_as_uint(c);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | key_low(hi >> 31, e));
+}
+__device__ __forceinline__ float key32_value(double key) {
+    return __uint_as_float(static_cast<uint32_t>(__builtin_bit_cast(uint64_t, key) >> 32));
+}
+
+// ---- within the G lanes of a token ---------------------------------------------------
+//
+// Each step pairs a lane with one of the other half of the lanes that hold the same by
+// then: neighbours, pairs, and the mirror images within 8 and 16 lanes.
+constexpr int kStep[4] = {0xB1, 0x4E, 0x141, 0x140};
+template <int G>
+constexpr int kSteps = G == 4 ? 2 : (G == 8 ? 3 : 4);
+
+template <int STEP>
+__device__ __forceinline__ int partner(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, kStep[STEP], 0xf, 0xf, true);
+}
+template <int STEP>
+__device__ __forceinline__ float partner(float v) {
+    return __builtin_bit_cast(float, partner<STEP>(__builtin_bit_cast(int, v)));
+}
+template <int STEP>
+__device__ __forceinline__ double partner(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = partner<STEP>(static_cast<int>(b)), hi = partner<STEP>(static_cast<int>(b >> 32));
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+// The token's lanes turned by I (which way does not matter to who takes all turns).
+template <int G, int I>
+__device__ __forceinline__ int turned(int v) {
+    if constexpr (G == 16) return __builtin_amdgcn_update_dpp(0, v, 0x120 + I, 0xf, 0xf, true);
+    else if constexpr (G == 4)
+        return __builtin_amdgcn_update_dpp(0, v, I | ((1 + I) & 3) << 2 | ((2 + I) & 3) << 4 | ((3 + I) & 3) << 6, 0xf, 0xf, true);
+    else return __shfl(v, (lane_id() & ~(G - 1)) | ((lane_id() + I) & (G - 1)), 64);
+}
+// How many of the token's other lanes have a larger key.
+template <int G, int I = 1>
+__device__ __forceinline__ int larger_keys(double key) {
+    if constexpr (I == G) return 0;
+    else {
+        const uint64_t b = __builtin_bit_cast(uint64_t, key);
+        const uint32_t lo = turned<G, I>(static_cast<int>(b)), hi = turned<G, I>(static_cast<int>(b >> 32));
+        return (__builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo) > key ? 1 : 0) + larger_keys<G, I + 1>(key);
+    }
+}
+template <int G, typename T, typename F>
+__device__ __forceinline__ T reduce(T v, F op) {
+    v = op(v, partner<0>(v));
+    v = op(v, partner<1>(v));
+    if constexpr (G >= 8) v = op(v, partner<2>(v));
+    if constexpr (G >= 16) v = op(v, partner<3>(v));
+    return v;
+}
+struct Max {
+    template <typename T>
+    __device__ __forceinline__ T operator()(T a, T b) const { return a > b ? a : b; }
+};
+struct Min {
+    template <typename T>
+    __device__ __forceinline__ T operator()(T a, T b) const { return a < b ? a : b; }
+};
+struct Add {
+    template <typename T>
+    __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
+};
+
+// ---- sorted lists of 8 keys, the largest first -------------------------------------
+
+__device__ __forceinline__ void order(double& a, double& b) {
+    const double x = key_max(a, b);
+    b = key_min(a, b);
+    a = x;
+}
+// (the 19 comparisons of Batcher's odd-even merge sort)
+__device__ __forceinline__ void sort8(double* v) {
+    order(v[0], v[1]); order(v[2], v[3]); order(v[4], v[5]); order(v[6], v[7]);
+    order(v[0], v[2]); order(v[1], v[3]); order(v[4], v[6]); order(v[5], v[7]);
+    order(v[1], v[2]); order(v[5], v[6]);
+    order(v[0], v[4]); order(v[1], v[5]); order(v[2], v[6]); order(v[3], v[7]);
+    order(v[2], v[4]); order(v[3], v[5]);
+    order(v[1], v[2]); order(v[3], v[4]); order(v[5], v[6]);
+}
+// The 8 largest of a and b (b the other way round: the larger of each pair are they,
+// first rising and then falling), sorted.
+__device__ __forceinline__ void merge8(double* a, const double* b) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = key_max(a[i], b[7 - i]);
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if ((i & d) == 0) order(a[i], a[i + d]);
+}
+template <int STEP>
+__device__ __forceinline__ void merge_partner(double* a) {
+    double b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = partner<STEP>(a[i]);
+    merge8(a, b);
+}
+
+// ---- a token's choice in 64 bits, by a whole wave ---------------------------------------
+
+// buf: 2 * MOE_MAX_EXPERTS doubles of LDS.  `l`, `s`: of the lane's experts.
+__device__ __forceinline__ void choose64(const moe_gating_t& g, const float* __restrict__ logits,
+                                         const float* __restrict__ bias, int64_t t, double* buf,
+                                         int32_t* __restrict__ ids, float* __restrict__ gates, double (&s)[kEpl]) {
+    const int lane = lane_id();
     const int E = g.E, k = g.k;
     const int size = E / g.groups;
     const bool limited = g.groups_kept < g.groups;
     const bool by_logit = bias == nullptr && (!limited || g.group_top == 1);
-    double* const c_of = s_c[wave];
-    double* const v_of = s_v[wave];
+    double l[kEpl], c[kEpl];
+    double top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kEpl; ++j) {
+        const int e = lane + 64 * j;
+        l[j] = e < E ? logits[t * E + e] : -INFINITY;
+        top = fmax(top, l[j]);
+    }
+    if (g.score == MOE_SCORE_SOFTMAX) {
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) top = fmax(top, __shfl_xor(top, off, 64));
+        double z = 0;
+#pragma unroll
+        for (int j = 0; j < kEpl; ++j) {
+            // (a row of minus infinities: all scores zero)
+            s[j] = top == -INFINITY || lane + 64 * j >= E ? 0 : exp(l[j] - top);
+            z += s[j];
+        }
+        z = wave_sum(z);
+#pragma unroll
+        for (int j = 0; j < kEpl; ++j) s[j] = z == 0 ? 0 : s[j] / z;
+    } else {
+#pragma unroll
+        for (int j = 0; j < kEpl; ++j) s[j] = lane + 64 * j < E ? 1.0 / (1.0 + exp(-l[j])) : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < kEpl; ++j) {
+        const int e = lane + 64 * j;
+        c[j] = by_logit ? l[j] : s[j] + (bias != nullptr && e < E ? bias[e] : 0.f);
+        // (a NaN comes last; an expert that is out has -DBL_MAX, below any that is not)
+        c[j] = c[j] == c[j] ? fmin(fmax(c[j], -1e308), 1e308) : -1e308;
+        if (e >= E) c[j] = -DBL_MAX;
+    }
+    if (limited) {
+        double* const c_of = buf;
+        double* const v_of = buf + MOE_MAX_EXPERTS;
+#pragma unroll
+        for (int j = 0; j < kEpl; ++j)
+            if (lane + 64 * j < E) c_of[lane + 64 * j] = c[j];
+        wave_lds();
+        for (int q = lane; q < g.groups; q += 64) {
+            double a = -DBL_MAX, b = -DBL_MAX;
+            for (int e = q * size; e < (q + 1) * size; ++e) {
+                const double v = c_of[e];
+                b = fmax(b, fmin(a, v));
+                a = fmax(a, v);
+            }
+            // (a sum with minus infinity is that)
+            v_of[q] = g.group_top == 2 && size > 1 ? fmax(a + b, -1e308) : a;
+        }
+        wave_lds();
+#pragma unroll
+        for (int j = 0; j < kEpl; ++j) {
+            const int e = lane + 64 * j;
+            if (e >= E) continue;
+            const int mine = e / size;
+            int rank = 0;
+            for (int q = 0; q < g.groups; ++q) rank += before(v_of[q], q, v_of[mine], mine) ? 1 : 0;
+            if (rank >= g.groups_kept) c[j] = -DBL_MAX;
+        }
+        wave_lds();
+    }
+    double my_s = 0;
+    int my_e = 0;
+    for (int r = 0; r < k; ++r) {
+        double m = c[0];
+#pragma unroll
+        for (int j = 1; j < kEpl; ++j) m = key_max(m, c[j]);
+        m = reduce<16>(m, [](double a, double b) { return key_max(a, b); });
+        const uint64_t bits = __builtin_bit_cast(uint64_t, m);
+        double row[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(bits), 16 * i);
+            const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(bits >> 32), 16 * i);
+            row[i] = __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+        }
+        m = key_max(key_max(row[0], row[1]), key_max(row[2], row[3]));
+        // the lowest expert that has it
+        int e = 0;
+#pragma unroll
+        for (int j = kEpl - 1; j >= 0; --j) {
+            const uint64_t has = __ballot(c[j] == m);
+            if (has != 0) e = 64 * j + __builtin_ctzll(has);
+        }
+        double ws = s[0];
+#pragma unroll
+        for (int j = 0; j < kEpl; ++j) {
+            if (e >> 6 == j) {
+                ws = s[j];
+                if (lane == (e & 63)) c[j] = -DBL_MAX;
+            }
+        }
+        ws = __shfl(ws, e & 63, 64);
+        if (lane == r) {
+            my_s = ws;
+            my_e = e;
+        }
+    }
+    const double total = wave_sum(my_s);
+    if (lane < k) {
+        ids[t * k + lane] = my_e;
+        const double v = g.renormalise ? (total == 0 ? 0 : my_s / total) : my_s;
+        gates[t * k + lane] = static_cast<float>(g.scale * v);
+    }
+}
+
+// Any k: a wave per token, its share of the tokens one after the other.
+__global__ __launch_bounds__(256) void route_scored_wave_kernel(moe_gating_t g, const float* __restrict__ logits,
+                                                               const float* __restrict__ bias,
+                                                               int32_t* __restrict__ ids, float* __restrict__ gates,
+                                                               float* __restrict__ partial) {
+    __shared__ double s_buf[4][2 * MOE_MAX_EXPERTS];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     double sum[kEpl] = {};
-    for (int i = 0; i < kTokens; ++i) {
-        const int64_t t = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * kTokens + i;
-        if (t >= g.T) break;
-        double l[kEpl], s[kEpl], c[kEpl];
-        double top = -INFINITY;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + wave; t < g.T; t += static_cast<int64_t>(gridDim.x) * 4) {
+        double s[kEpl];
+        choose64(g, logits, bias, t, s_buf[wave], ids, gates, s);
 #pragma unroll
-        for (int j = 0; j < kEpl; ++j) {
-            const int e = lane + 64 * j;
-            l[j] = e < E ? logits[t * E + e] : -INFINITY;
-            top = fmax(top, l[j]);
-        }
-        if (g.score == MOE_SCORE_SOFTMAX) {
-            top = wave_max(top);
-            double z = 0;
-#pragma unroll
-            for (int j = 0; j < kEpl; ++j) {
-                // (a row of minus infinities: all scores zero)
-                s[j] = top == -INFINITY ? 0 : exp(l[j] - top);
-                z += lane + 64 * j < E ? s[j] : 0;
-            }
-            z = wave_sum(z);
-#pragma unroll
-            for (int j = 0; j < kEpl; ++j) s[j] = z == 0 ? 0 : s[j] / z;
-        } else {
-#pragma unroll
-            for (int j = 0; j < kEpl; ++j) s[j] = 1.0 / (1.0 + exp(-l[j]));
-        }
-        bool live[kEpl];
-#pragma unroll
-        for (int j = 0; j < kEpl; ++j) {
-            const int e = lane + 64 * j;
-            live[j] = e < E;
-            c[j] = by_logit ? l[j] : s[j] + (bias != nullptr && e < E ? bias[e] : 0.f);
-            if (!(c[j] == c[j])) c[j] = -INFINITY;  // (a NaN comes last)
-            if (live[j]) sum[j] += s[j];
-        }
-        if (limited) {
-#pragma unroll
-            for (int j = 0; j < kEpl; ++j)
-                if (live[j]) c_of[lane + 64 * j] = c[j];
-            __builtin_amdgcn_wave_barrier();
-            for (int q = lane; q < g.groups; q += 64) {
-                double a = -INFINITY, b = -INFINITY;
-                for (int e = q * size; e < (q + 1) * size; ++e) {
-                    const double v = c_of[e];
-                    b = fmax(b, fmin(a, v));
-                    a = fmax(a, v);
-                }
-                const double v = g.group_top == 2 && size > 1 ? a + b : a;
-                v_of[q] = v == v ? v : -INFINITY;
-            }
-            __builtin_amdgcn_wave_barrier();
-#pragma unroll
-            for (int j = 0; j < kEpl; ++j) {
-                if (!live[j]) continue;
-                const int mine = (lane + 64 * j) / size;
-                int rank = 0;
-                for (int q = 0; q < g.groups; ++q) rank += before(v_of[q], q, v_of[mine], mine) ? 1 : 0;
-                live[j] = rank < g.groups_kept;
-            }
-        }
-        double my_s = 0;
-        int my_e = 0;
-        for (int r = 0; r < k; ++r) {
-            double bv = -INFINITY, bs = 0;
-            int be = INT_MAX;
-#pragma unroll
-            for (int j = 0; j < kEpl; ++j) {
-                const int e = lane + 64 * j;
-                if (live[j] && (be == INT_MAX || before(c[j], e, bv, be))) {
-                    bv = c[j];
-                    be = e;
-                    bs = s[j];
-                }
-            }
-#pragma unroll
-            for (int off = 32; off > 0; off >>= 1) {
-                const double ov = __shfl_xor(bv, off, 64), os = __shfl_xor(bs, off, 64);
-                const int oe = __shfl_xor(be, off, 64);
-                if (oe != INT_MAX && (be == INT_MAX || before(ov, oe, bv, be))) {
-                    bv = ov;
-                    be = oe;
-                    bs = os;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < kEpl; ++j)
-                if (lane + 64 * j == be) live[j] = false;
-            if (lane == r) {
-                my_s = bs;
-                my_e = be;
-            }
-        }
-        const double total = wave_sum(my_s);
-        if (lane < k) {
-            ids[t * k + lane] = my_e;
-            const double v = g.renormalise ? (total == 0 ? 0 : my_s / total) : my_s;
-            gates[t * k + lane] = static_cast<float>(g.scale * v);
-        }
-        __builtin_amdgcn_wave_barrier();
+        for (int j = 0; j < kEpl; ++j) sum[j] += s[j];
     }
     if (partial == nullptr) return;
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kEpl; ++j) s_c[wave][lane + 64 * j] = sum[j];
+    for (int j = 0; j < kEpl; ++j) s_buf[wave][lane + 64 * j] = sum[j];
     __syncthreads();
     const int e = threadIdx.x;
-    if (e < E)
-        partial[static_cast<int64_t>(blockIdx.x) * E + e] =
-            static_cast<float>((s_c[0][e] + s_c[1][e]) + (s_c[2][e] + s_c[3][e]));
+    if (e < g.E)
+        partial[static_cast<int64_t>(blockIdx.x) * g.E + e] =
+            static_cast<float>((s_buf[0][e] + s_buf[1][e]) + (s_buf[2][e] + s_buf[3][e]));
 }
 
-// sums[e] = the sum of the blocks' partial sums, in a fixed order.
-__global__ __launch_bounds__(256) void score_sums_kernel(const float* __restrict__ partial, int64_t blocks, int E,
-                                                        float* __restrict__ sums) {
-    __shared__ double s[256];
-    double v = 0;
-    for (int64_t b = threadIdx.x; b < blocks; b += 256) v += partial[b * E + blockIdx.x];
-    s[threadIdx.x] = v;
-    __syncthreads();
-    for (int off = 128; off > 0; off >>= 1) {
-        if (threadIdx.x < off) s[threadIdx.x] += s[threadIdx.x + off];
+// ---- a token's choice in 32 bits, by G lanes ------------------------------------------------
+//
+// Lane s of a token has the EPL experts from EPL * s on.  Each lane sorts its 8
+// largest keys, and the lists are merged over the lanes.  Groups that are whole lanes (a
+// power of two of them) are valued by the heads of the lists, and the lists of groups that
+// go are dropped; other groups are valued from LDS before the lists are made.
+//
+// Errors: exp2 of the rounded product l log2(e), and the reciprocal, leave s with an
+// absolute error below 2^-21 max s (s |l| and s |l - max| are below 1 / e of it; the
+// softmax's sum adds 20 roundings to all of a token's s alike, which with a bias counts as
+// 2^-19.6 max s), the sum with the bias below 2^-24 |c|.  A choice is taken for certain if
+// all that it compared differs by more than 2^-18 max s + 2^-21 max |c| (twice that for
+// sums of two), else made again in 64 bits.
+//
+// 32768 tokens, 256 experts: see the launch below.
+constexpr int kMaxRounds = 32;  // of tokens that a workgroup takes one after the other
+constexpr float kLog2e = 1.44269504088896340736f;
+
+template <int G, int EPL, bool VEC>
+__global__ __launch_bounds__(256, 3) void route_scored_kernel(moe_gating_t g, const float* __restrict__ logits,
+                                                          const float* __restrict__ bias, int32_t* __restrict__ ids,
+                                                          float* __restrict__ gates, float* __restrict__ partial) {
+    constexpr int TPW = 64 / G;              // tokens per wave
+    constexpr int EMAX = G * EPL;
+    // a wave's LDS: c and the groups' values of its tokens, or choose64's, or (of all
+    // waves together) the score sums
+    constexpr int BUF = TPW * EMAX > 2 * MOE_MAX_EXPERTS ? TPW * EMAX : 2 * MOE_MAX_EXPERTS;
+    __shared__ double s_buf[4][BUF];
+    __shared__ uint64_t s_again[4][kMaxRounds];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int row = lane / G, s_lane = lane % G;
+    const int E = g.E, k = g.k;
+    const int size = E / g.groups;
+    const bool limited = g.groups_kept < g.groups;
+    const bool by_logit = bias == nullptr && (!limited || g.group_top == 1);
+    const int per_group = size / EPL;        // lanes of a group
+    const bool whole_lanes = limited && size % EPL == 0 && (per_group & (per_group - 1)) == 0;
+    const int e0 = s_lane * EPL;
+    float sum[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) sum[i] = 0.f;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * 4 * TPW;
+    const int64_t first = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * TPW;
+    int round = 0;                           // (at most kMaxRounds)
+    for (int64_t t0 = first; t0 < g.T; t0 += step, ++round) {
+        const bool has = t0 + row < g.T;
+        // (lanes past the last token work on it once more and store nothing)
+        const int64_t t = has ? t0 + row : g.T - 1;
+        const float* const from = logits + t * E;
+        float c[EPL], s[EPL];
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < EPL; i += 4) {
+                const float4 v = e0 + i < E ? *reinterpret_cast<const float4*>(from + e0 + i)
+                                            : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                c[i] = v.x;
+                c[i + 1] = v.y;
+                c[i + 2] = v.z;
+                c[i + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) c[i] = e0 + i < E ? from[e0 + i] : -INFINITY;
+        }
+        // scores (experts past the last: zero)
+        float top = -INFINITY, inv = 1.f, s_max = 1.f;
+        if (g.score == MOE_SCORE_SOFTMAX) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) top = fmaxf(top, c[i]);
+            top = reduce<G>(top, Max());
+            const float shift = top == -INFINITY ? 0.f : top;
+            float z = 0.f;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                s[i] = __builtin_amdgcn_exp2f((c[i] - shift) * kLog2e);
+                z += s[i];
+            }
+            z = reduce<G>(z, Add());
+            inv = z == 0.f ? 0.f : 1.f / z;
+            s_max = inv;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) s[i] *= inv;
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) s[i] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-c[i] * kLog2e));
+        }
+        if (partial != nullptr && has) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) sum[i] += s[i];
+        }
+        if (!by_logit) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) c[i] = s[i] + (bias != nullptr && e0 + i < E ? bias[e0 + i] : 0.f);
+        }
+        bool sure = true;
+        bool dropped = false;                // the lane's experts are out
+        uint32_t gone = 0;                   // bit i: expert e0 + i is out
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) gone |= (e0 + i < E ? 0u : 1u) << i;
+        float* const c_of = reinterpret_cast<float*>(s_buf[wave]) + row * EMAX;
+        float* const v_of = reinterpret_cast<float*>(s_buf[wave]) + TPW * EMAX + row * EMAX;
+        // the groups that stay differ from those that go by more than the error
+        auto apart = [&](float low, float high, float most) {
+            low = reduce<G>(low, Min());
+            high = reduce<G>(high, Max());
+            most = reduce<G>(most, Max());
+            return low - high > 2.f * (0x1p-18f * s_max + 0x1p-21f * most);
+        };
+        if (limited && !whole_lanes) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                if (e0 + i < E) c_of[e0 + i] = c[i] == c[i] ? c[i] : -INFINITY;
+            wave_lds();
+            float most = 0.f;
+            for (int q = s_lane; q < g.groups; q += G) {
+                float a = -INFINITY, a2 = -INFINITY;
+                for (int i = 0; i < size; ++i) {
+                    const float v = c_of[q * size + i];
+                    a2 = fmaxf(a2, fminf(a, v));
+                    a = fmaxf(a, v);
+                }
+                const float v = g.group_top == 2 && size > 1 ? a + a2 : a;
+                v_of[q] = v == v ? v : -INFINITY;
+                most = fmaxf(most, fmaxf(fabsf(a), size > 1 ? fabsf(a2) : 0.f));
+            }
+            wave_lds();
+            float low = INFINITY, high = -INFINITY;
+            uint32_t stay[(EMAX + 32 * G - 1) / (32 * G)] = {};   // bit i: group s_lane + G * i
+            int n = 0;
+            for (int q = s_lane; q < g.groups; q += G, ++n) {
+                const float v = v_of[q];
+                int rank = 0;
+                for (int o = 0; o < g.groups; ++o) rank += v_of[o] > v || (v_of[o] == v && o < q) ? 1 : 0;
+                if (rank < g.groups_kept) {
+                    stay[n / 32] |= 1u << (n & 31);
+                    low = fminf(low, v);
+                } else {
+                    high = fmaxf(high, v);
+                }
+            }
+            wave_lds();
+            n = 0;
+            for (int q = s_lane; q < g.groups; q += G, ++n) v_of[q] = stay[n / 32] >> (n & 31) & 1 ? 1.f : 0.f;
+            wave_lds();
+            int q = e0 / size, r = e0 - q * size;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                if (e0 + i < E && v_of[q] == 0.f) gone |= 1u << i;
+                if (++r == size) {
+                    r = 0;
+                    ++q;
+                }
+            }
+            wave_lds();
+            if (!by_logit) sure = apart(low, high, most);
+        }
+        double list[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) list[i] = gone >> i & 1 ? out_key(e0 + i) : key32(c[i], e0 + i);
+        sort8(list);
+        if constexpr (EPL == 16) {
+            sort8(list + 8);
+            merge8(list, list + 8);
+        }
+        if (whole_lanes) {
+            // the group's two largest, from the lists' heads
+            const bool live = e0 < E;
+            float a = live ? key32_value(list[0]) : -INFINITY, a2 = live ? key32_value(list[1]) : -INFINITY;
+            auto join = [&](float p, float p2) {
+                a2 = fmaxf(fminf(a, p), fmaxf(a2, p2));
+                a = fmaxf(a, p);
+            };
+            if (per_group >= 2) join(partner<0>(a), partner<0>(a2));
+            if (per_group >= 4) join(partner<1>(a), partner<1>(a2));
+            if constexpr (G >= 8) {
+                if (per_group >= 8) join(partner<2>(a), partner<2>(a2));
+            }
+            float v = g.group_top == 2 ? a + a2 : a;
+            // (the group's number, counted from the token's first lane)
+            const int q = s_lane / per_group;
+            const double mine = live ? key32(v, q) : out_key(q);
+            v = key32_value(key32(v, q));
+            const int better = larger_keys<G>(mine);
+            dropped = better >= g.groups_kept * per_group;
+            if (!by_logit)
+                sure = apart(live && !dropped ? v : INFINITY, live && dropped ? v : -INFINITY,
+                             live ? fmaxf(fabsf(a), fabsf(a2)) : 0.f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) list[i] = dropped ? out_key(e0 + i) : list[i];
+        }
+        merge_partner<0>(list);
+        merge_partner<1>(list);
+        if constexpr (G >= 8) merge_partner<2>(list);
+        if constexpr (G >= 16) merge_partner<3>(list);
+        // list: the token's 8 largest, in every lane
+        if (!by_logit) {
+            float last = 0.f, most = 0.f;
+            float gap = INFINITY;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float v = key32_value(list[j]);
+                if (j < k) {
+                    if (j > 0) gap = fminf(gap, last - v);
+                    most = fmaxf(most, fabsf(v));
+                    if (!(v > -INFINITY)) gap = 0.f;  // (differences of infinities are no numbers)
+                    last = v;
+                }
+            }
+            const float tol = 0x1p-18f * s_max + 0x1p-21f * most;
+            // no others within the error of the last
+            int near = 0;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) near += !(gone >> i & 1) && !(c[i] < last - tol) ? 1 : 0;
+            near = reduce<G>(dropped ? 0 : near, Add());
+            sure = sure && gap > tol && near <= k;
+        }
+        // gates: lane j has slot j (and j + G)
+        constexpr int SLOTS = G >= 8 ? 1 : 2;
+        float chosen[SLOTS];
+        int id[SLOTS];
+        float total = 0.f;
+#pragma unroll
+        for (int u = 0; u < SLOTS; ++u) {
+            double mine = list[0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) mine = s_lane + u * G == j ? list[j] : mine;
+            id[u] = key_index(mine);
+            chosen[u] = 0.f;
+            if (s_lane + u * G < k) {
+                const float l = from[min(id[u], E - 1)];
+                if (g.score == MOE_SCORE_SOFTMAX) chosen[u] = expf(l - (top == -INFINITY ? 0.f : top)) * inv;
+                else chosen[u] = 1.f / (1.f + expf(-l));
+            }
+            total += chosen[u];
+        }
+        total = reduce<G>(total, Add());
+        if (has && sure) {
+#pragma unroll
+            for (int u = 0; u < SLOTS; ++u) {
+                const int j = s_lane + u * G;
+                if (j >= k) continue;
+                ids[t * k + j] = id[u];
+                const float v = g.renormalise ? (total == 0.f ? 0.f : chosen[u] / total) : chosen[u];
+                gates[t * k + j] = g.scale * v;
+            }
+        }
+        const uint64_t unsure = __ballot(has && !sure && s_lane == 0);
+        if (lane == 0) s_again[wave][round] = unsure;
+    }
+    if (partial != nullptr) {
+        // over the wave's tokens, then over the waves
+        float* const w_sum = reinterpret_cast<float*>(s_buf);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            float v = sum[i];
+#pragma unroll
+            for (int off = G; off < 64; off <<= 1) v += __shfl_xor(v, off, 64);
+            if (row == 0) w_sum[wave * EMAX + e0 + i] = v;
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < E; e += 256)
+            partial[static_cast<int64_t>(blockIdx.x) * E + e] =
+                (w_sum[e] + w_sum[EMAX + e]) + (w_sum[2 * EMAX + e] + w_sum[3 * EMAX + e]);
         __syncthreads();
     }
-    if (threadIdx.x == 0) sums[blockIdx.x] = static_cast<float>(s[0]);
+    // the tokens whose choice is not certain, again (here, where no registers are held)
+    wave_lds();
+    for (int r = 0; r < round; ++r) {
+        uint64_t again = s_again[wave][r];
+        while (again != 0) {
+            const int at = __builtin_ctzll(again);
+            again &= again - 1;
+            double unused[kEpl];
+            choose64(g, logits, bias, first + r * step + at / G, s_buf[wave], ids, gates, unused);
+        }
+    }
 }
 
-// The gradient: with r_j = s_j / S (S the sum of the chosen s) the chosen expert
-// j's score has the derivative
-//   renormalised  scale (dg_j - sum_i r_i dg_i) / S       otherwise  scale dg_j
-// and every score that of its sum; then
-//   sigmoid  dl = ds s (1 - s)          softmax  dl = s (ds - sum_i s_i ds_i)
-// where s_j / S is taken as one quotient (1 / S may overflow).  One wave per token.
-template <typename O>
+// sums[e] = the sum of the blocks' partial sums, in a fixed order: 32 experts per
+// workgroup, 8 threads each.
+__global__ __launch_bounds__(256) void score_sums_kernel(const float* __restrict__ partial, int64_t blocks, int E,
+                                                        float* __restrict__ sums) {
+    __shared__ double s[8][33];
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const int e = blockIdx.x * 32 + x;
+    double v = 0;
+    if (e < E) {
+#pragma unroll 8
+        for (int64_t b = y; b < blocks; b += 8) v += partial[b * E + e];
+    }
+    s[y][x] = v;
+    __syncthreads();
+    if (y == 0 && e < E) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) v += s[i][x];
+        sums[e] = static_cast<float>(v);
+    }
+}
+
+// ---- the gradient ------------------------------------------------------------------------
+//
+// With r_j = s_j / S (S the sum of the chosen s) slot j's share of s ds is
+//   renormalised  u_j = scale r_j (dg_j - sum_i r_i dg_i)      otherwise  scale s_j dg_j
+// and with ds = dscore_sums
+//   sigmoid  dl_e = (u_e + s_e ds_e) (1 - s_e)
+//   softmax  dl_e = u_e + s_e (ds_e - sum_i s_i ds_i - sum_j u_j)
+// (s_j / S is one quotient: 1 / S may overflow; renormalised, the u_j add up to zero).
+//
+// G lanes per token, 8 experts each; lane j takes slots j, j + G, .. and leaves u in LDS
+// under its expert.  Bound by the logits read and the gradients written: whole 16-byte
+// words, two tokens of 256 experts in flight per wave.  Without dscore_sums all but the
+// chosen experts' gradients are zero (softmax: if renormalised), and only their logits
+// are read.
+template <int G, typename T, typename F>
+__device__ __forceinline__ T reduce_wide(T v, F op) {
+    v = reduce<(G < 16 ? G : 16)>(v, op);
+    if constexpr (G >= 32) v = op(v, __shfl_xor(v, 16, 64));
+    return v;
+}
+
+// s and 1 - s of a logit, neither by a difference.
+__device__ __forceinline__ void sigmoid_parts(float l, float& s, float& rest) {
+    const float x = expf(-fabsf(l)), p = __builtin_amdgcn_rcpf(1.f + x);
+    s = l >= 0.f ? p : x * p;
+    rest = l >= 0.f ? x * p : p;
+    if (!(l == l)) s = rest = l;
+}
+
+template <int G, bool VEC, typename O>
 __global__ __launch_bounds__(256) void route_scored_backward_kernel(moe_gating_t g, const float* __restrict__ logits,
                                                                    const int32_t* __restrict__ ids,
                                                                    const float* __restrict__ dgates,
                                                                    const float* __restrict__ dsums,
                                                                    O* __restrict__ dlogits) {
-    const int lane = threadIdx.x & 63;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-    if (t >= g.T) return;
+    constexpr int N = 8, TPW = 64 / G;
+    __shared__ __attribute__((aligned(16))) float s_u[4][TPW * G * N];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int row = lane / G, s_lane = lane % G;
     const int E = g.E, k = g.k;
-    float s[kEpl], rest[kEpl], l[kEpl], ds[kEpl], dg[kEpl];
-    bool hit[kEpl];
-    float top = -INFINITY;
+    const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * TPW;
+    if (t0 >= g.T) return;
+    const bool has = t0 + row < g.T;
+    const int64_t t = has ? t0 + row : g.T - 1;
+    const bool softmax = g.score == MOE_SCORE_SOFTMAX;
+    const bool sparse = dsums == nullptr && (!softmax || g.renormalise);
+    const float* const from = logits + t * E;
+    float* const u_of = s_u[wave] + row * G * N;
+    // expert i of the lane
+    auto expert = [&](int i) { return VEC ? 4 * (s_lane + G * (i / 4)) + i % 4 : s_lane + G * i; };
+    float l[N], ds[N];
 #pragma unroll
-    for (int j = 0; j < kEpl; ++j) {
-        const int e = lane + 64 * j;
-        l[j] = e < E ? logits[t * E + e] : -INFINITY;
-        top = fmaxf(top, l[j]);
-        ds[j] = dsums != nullptr && e < E ? dsums[e] : 0.f;
-        dg[j] = 0.f;
-        hit[j] = false;
+    for (int i = 0; i < N; ++i) {
+        l[i] = -INFINITY;
+        ds[i] = 0.f;
     }
-    if (g.score == MOE_SCORE_SOFTMAX) {
+    if (!sparse) {
+        if constexpr (VEC) {
 #pragma unroll
-        for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+            for (int i = 0; i < N; i += 4)
+                if (expert(i) < E) {
+                    const float4 v = *reinterpret_cast<const float4*>(from + expert(i));
+                    l[i] = v.x;
+                    l[i + 1] = v.y;
+                    l[i + 2] = v.z;
+                    l[i + 3] = v.w;
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (expert(i) < E) l[i] = from[expert(i)];
+        }
+        if (dsums != nullptr) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (expert(i) < E) ds[i] = dsums[expert(i)];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) u_of[s_lane + G * i] = 0.f;
+    // the slots: up to MOE_MAX_TOPK / G of them per lane
+    constexpr int SLOTS = (MOE_MAX_TOPK + G - 1) / G;
+    int id[SLOTS];
+    float dg[SLOTS], lc[SLOTS];
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j) {
+        const int at = s_lane + G * j;
+        id[j] = at < k ? ids[t * k + at] : -1;
+        if (id[j] >= E) id[j] = -1;
+        dg[j] = at < k ? g.scale * dgates[t * k + at] : 0.f;
+        lc[j] = id[j] >= 0 ? from[id[j]] : -INFINITY;
+    }
+    // scores
+    float top = -INFINITY, inv = 0.f;
+    float s[N], rest[N];
+    if (softmax) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) top = fmaxf(top, l[i]);
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j) top = fmaxf(top, lc[j]);
+        top = reduce_wide<G>(top, Max());
+        if (top == -INFINITY) top = 0.f;
         float z = 0.f;
 #pragma unroll
-        for (int j = 0; j < kEpl; ++j) {
-            s[j] = top == -INFINITY || lane + 64 * j >= E ? 0.f : expf(l[j] - top);
-            z += s[j];
+        for (int i = 0; i < N; ++i) {
+            s[i] = expf(l[i] - top);
+            z += s[i];
         }
-        z = wave_sum(z);
+        z = reduce_wide<G>(z, Add());
+        // (sparse: the chosen experts' shares do not depend on it)
+        inv = sparse ? 1.f : (z == 0.f ? 0.f : 1.f / z);
 #pragma unroll
-        for (int j = 0; j < kEpl; ++j) s[j] = z == 0.f ? 0.f : s[j] / z;
+        for (int i = 0; i < N; ++i) {
+            s[i] *= inv;
+            rest[i] = 0.f;
+        }
     } else {
 #pragma unroll
-        for (int j = 0; j < kEpl; ++j) {
-            s[j] = lane + 64 * j < E ? 1.f / (1.f + expf(-l[j])) : 0.f;
-            rest[j] = 1.f / (1.f + expf(l[j]));
+        for (int i = 0; i < N; ++i) {
+            sigmoid_parts(l[i], s[i], rest[i]);
+            if (sparse) s[i] = 0.f;
         }
     }
-    for (int i = 0; i < k; ++i) {
-        const int e = ids[t * k + i];
-        const float v = g.scale * dgates[t * k + i];
+    float sc[SLOTS], u[SLOTS], restc[SLOTS], total = 0.f, mean = 0.f, all = 0.f;
 #pragma unroll
-        for (int j = 0; j < kEpl; ++j)
-            if (lane + 64 * j == e) {
-                dg[j] += v;
-                hit[j] = true;
-            }
+    for (int j = 0; j < SLOTS; ++j) {
+        restc[j] = 1.f;
+        if (softmax) sc[j] = expf(lc[j] - top) * inv;
+        else sigmoid_parts(lc[j], sc[j], restc[j]);
+        if (id[j] < 0) sc[j] = 0.f;
+        total += sc[j];
     }
-    // u: the chosen experts' share of s ds
-    float u[kEpl], total = 0.f;
-#pragma unroll
-    for (int j = 0; j < kEpl; ++j) total += hit[j] ? s[j] : 0.f;
     if (g.renormalise) {
-        total = wave_sum(total);
-        float mean = 0.f;
+        total = reduce_wide<G>(total, Add());
 #pragma unroll
-        for (int j = 0; j < kEpl; ++j) {
-            u[j] = hit[j] && total != 0.f ? s[j] / total : 0.f;
-            mean += u[j] * dg[j];
+        for (int j = 0; j < SLOTS; ++j) {
+            sc[j] = total == 0.f ? 0.f : sc[j] / total;
+            mean += sc[j] * dg[j];
         }
-        mean = wave_sum(mean);
+        mean = reduce_wide<G>(mean, Add());
+    }
 #pragma unroll
-        for (int j = 0; j < kEpl; ++j) u[j] *= dg[j] - mean;
+    for (int j = 0; j < SLOTS; ++j) {
+        u[j] = sc[j] * (dg[j] - mean);
+        if (!g.renormalise) all += u[j];
+    }
+    wave_lds();
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j)
+        if (id[j] >= 0) atomicAdd(u_of + id[j], sparse ? u[j] * restc[j] : u[j]);  // (a slot each, but for repeated experts)
+    if (softmax) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) all += s[i] * ds[i];
+        all = reduce_wide<G>(all, Add());
+    }
+    wave_lds();
+    if (!has) return;
+    O* const out = dlogits + t * E;
+    float v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float ue = u_of[VEC ? 4 * (s_lane + G * (i / 4)) + i % 4 : s_lane + G * i];
+        v[i] = sparse ? ue : (softmax ? ue + s[i] * (ds[i] - all) : (ue + s[i] * ds[i]) * rest[i]);
+    }
+    if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            if (expert(i) >= E) continue;
+            if constexpr (sizeof(O) == 4)
+                *reinterpret_cast<float4*>(out + expert(i)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            else
+                *reinterpret_cast<uint2*>(out + expert(i)) = make_uint2(pack_bf16x2(v[i], v[i + 1]), pack_bf16x2(v[i + 2], v[i + 3]));
+        }
     } else {
 #pragma unroll
-        for (int j = 0; j < kEpl; ++j) u[j] = hit[j] ? s[j] * dg[j] : 0.f;
-    }
-    float mean = 0.f;
-    if (g.score == MOE_SCORE_SOFTMAX) {
-        // (renormalised, the chosen shares add up to zero)
-#pragma unroll
-        for (int j = 0; j < kEpl; ++j) mean += s[j] * ds[j] + (g.renormalise ? 0.f : u[j]);
-        mean = wave_sum(mean);
-    }
-#pragma unroll
-    for (int j = 0; j < kEpl; ++j) {
-        const int e = lane + 64 * j;
-        const float v = g.score == MOE_SCORE_SOFTMAX ? u[j] + s[j] * (ds[j] - mean) : (u[j] + s[j] * ds[j]) * rest[j];
-        if (e < E) dlogits[t * E + e] = static_cast<O>(v);
+        for (int i = 0; i < N; ++i)
+            if (expert(i) < E) out[expert(i)] = static_cast<O>(v[i]);
     }
 }
 
 }  // namespace
 
-int64_t route_scored_blocks(const moe_gating_t& g) { return ceil_div(g.T, 4 * kTokens); }
+namespace {
+
+// Lanes per token and experts per lane of the 32-bit choice: the fewest lanes that
+// hold the experts, 8 each, 16 each beyond 128 (wider lists, fewer steps between lanes).
+int lanes_for(int E) { return E <= 32 ? 4 : (E <= 64 ? 8 : 16); }
+
+}  // namespace
+
+// Workgroups: one round of tokens each up to 512 of them, then up to kMaxRounds
+// (each lane adds that many scores in 32 bits).
+int64_t route_scored_blocks(const moe_gating_t& g) {
+    const int64_t per_round = g.k <= 8 ? 4 * (64 / lanes_for(g.E)) : 4;
+    const int64_t rounds = ceil_div(g.T, per_round);
+    return std::max(std::min<int64_t>(rounds, 512), ceil_div(rounds, kMaxRounds));
+}
 
 hipError_t launch_route_scored(const moe_gating_t& g, const float* logits, const float* bias, int32_t* ids,
                                float* gates, float* score_sums, float* partial, hipStream_t s) {
+    // (without sums nothing is gained by more than one round per workgroup)
     const int64_t blocks = route_scored_blocks(g);
-    if (blocks > 0)
-        route_scored_kernel<<<static_cast<unsigned>(blocks), 256, 0, s>>>(g, logits, bias, ids, gates,
-                                                                          score_sums != nullptr ? partial : nullptr);
-    if (score_sums != nullptr) score_sums_kernel<<<static_cast<unsigned>(g.E), 256, 0, s>>>(partial, blocks, g.E, score_sums);
+    float* const sums = score_sums != nullptr ? partial : nullptr;
+    if (blocks > 0) {
+        const unsigned grid = static_cast<unsigned>(blocks);
+        const bool vec = g.E % 4 == 0;
+#define MOE_ROUTE(G, EPL)                                                                                      \
+    do {                                                                                                       \
+        if (vec) route_scored_kernel<G, EPL, true><<<grid, 256, 0, s>>>(g, logits, bias, ids, gates, sums);      \
+        else route_scored_kernel<G, EPL, false><<<grid, 256, 0, s>>>(g, logits, bias, ids, gates, sums);         \
+    } while (0)
+        if (g.k > 8) route_scored_wave_kernel<<<grid, 256, 0, s>>>(g, logits, bias, ids, gates, sums);
+        else if (g.E <= 32) MOE_ROUTE(4, 8);
+        else if (g.E <= 64) MOE_ROUTE(8, 8);
+        else if (g.E <= 128) MOE_ROUTE(16, 8);
+        else MOE_ROUTE(16, 16);
+#undef MOE_ROUTE
+    }
+    if (score_sums != nullptr)
+        score_sums_kernel<<<static_cast<unsigned>(ceil_div(g.E, 32)), 256, 0, s>>>(partial, blocks, g.E, score_sums);
     return hipGetLastError();
 }
+
+namespace {
+
+template <typename O>
+void start_backward(const moe_gating_t& g, const float* logits, const int32_t* ids, const float* dgates,
+                    const float* dsums, O* dlogits, hipStream_t s) {
+    const int lanes = g.E <= 32 ? 4 : (g.E <= 64 ? 8 : (g.E <= 128 ? 16 : 32));
+    const unsigned grid = static_cast<unsigned>(ceil_div(g.T, 4 * (64 / lanes)));
+    const bool vec = g.E % 4 == 0;
+#define MOE_BACK(G)                                                                                              \
+    do {                                                                                                         \
+        if (vec) route_scored_backward_kernel<G, true><<<grid, 256, 0, s>>>(g, logits, ids, dgates, dsums, dlogits); \
+        else route_scored_backward_kernel<G, false><<<grid, 256, 0, s>>>(g, logits, ids, dgates, dsums, dlogits);    \
+    } while (0)
+    switch (lanes) {
+        case 4: MOE_BACK(4); break;
+        case 8: MOE_BACK(8); break;
+        case 16: MOE_BACK(16); break;
+        default: MOE_BACK(32); break;
+    }
+#undef MOE_BACK
+}
+
+}  // namespace
 
 hipError_t launch_route_scored_backward(const moe_gating_t& g, const float* logits, const int32_t* ids,
                                         const float* dgates, const float* dscore_sums, int dtype, void* dlogits,
                                         hipStream_t s) {
-    const unsigned grid = static_cast<unsigned>(ceil_div(g.T, 4));
     if (dtype == MOE_DTYPE_BF16)
-        route_scored_backward_kernel<<<grid, 256, 0, s>>>(g, logits, ids, dgates, dscore_sums,
-                                                          static_cast<__bf16*>(dlogits));
+        start_backward(g, logits, ids, dgates, dscore_sums, static_cast<__bf16*>(dlogits), s);
     else
-        route_scored_backward_kernel<<<grid, 256, 0, s>>>(g, logits, ids, dgates, dscore_sums,
-                                                          static_cast<float*>(dlogits));
+        start_backward(g, logits, ids, dgates, dscore_sums, static_cast<float*>(dlogits), s);
     return hipGetLastError();
 }
 
