@@ -8,6 +8,8 @@
 // And its gradient:
 //   dy_perm[assign_pos[t*k + j], :] = gates[t, j] * dy[t, :]
 //   dgates[t, j] = sum_c dy[t, c] * y_perm[assign_pos[t*k + j], c]
+#include <type_traits>
+
 #include "device_util.h"
 #include "moe_internal.h"
 
@@ -114,11 +116,25 @@ __global__ __launch_bounds__(256) void combine_f32_kernel(const float* __restric
 // One workgroup per token: a thread keeps its columns of dy, and of KM slots at a
 // time reads y_perm's rows, adds to the slots' products and writes dy_perm's rows.
 // The products' sums over the workgroup are taken at the end, in a fixed order.
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+// Rows read and written once go past the caches.
+__device__ __forceinline__ void store_nt(uint4* p, const uint4& v) {
+    const u32x4_t w = {v.x, v.y, v.z, v.w};
+    __builtin_nontemporal_store(w, reinterpret_cast<u32x4_t*>(p));
+}
+__device__ __forceinline__ void store_nt(float4* p, const float4& v) {
+    const f32x4_t w = {v.x, v.y, v.z, v.w};
+    __builtin_nontemporal_store(w, reinterpret_cast<f32x4_t*>(p));
+}
+__device__ __forceinline__ void store_nt(float* p, float v) { __builtin_nontemporal_store(v, p); }
+
 template <typename T, int V>
 struct Chunk;  // V values
 template <>
 struct Chunk<bf16_t, 8> {
     using Raw = uint4;
+    static __device__ __forceinline__ uint4 load(const uint4* p) { return load_nt(p); }
     static __device__ __forceinline__ void unpack(const uint4& w, float (&v)[8]) {
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -135,6 +151,10 @@ struct Chunk<bf16_t, 8> {
 template <>
 struct Chunk<float, 4> {
     using Raw = float4;
+    static __device__ __forceinline__ float4 load(const float4* p) {
+        const f32x4_t v = load_nt(reinterpret_cast<const f32x4_t*>(p));
+        return make_float4(v.x, v.y, v.z, v.w);
+    }
     static __device__ __forceinline__ void unpack(const float4& w, float (&v)[4]) {
         v[0] = w.x;
         v[1] = w.y;
@@ -148,6 +168,7 @@ struct Chunk<float, 4> {
 template <>
 struct Chunk<float, 1> {
     using Raw = float;
+    static __device__ __forceinline__ float load(const float* p) { return load_nt(p); }
     static __device__ __forceinline__ void unpack(const float& w, float (&v)[1]) { v[0] = w; }
     static __device__ __forceinline__ float scaled(const float (&v)[1], float g) { return g * v[0]; }
 };
@@ -173,6 +194,12 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(
         }
         for (int c = threadIdx.x; c < chunks; c += 256) {
             float a[V];
+            typename C::Raw y[KM];
+            if (dgates != nullptr) {
+#pragma unroll
+                for (int j = 0; j < KM; ++j)
+                    if (pos[j] >= 0) y[j] = C::load(y_perm + static_cast<int64_t>(pos[j]) * chunks + c);
+            }
             C::unpack(dy[t * chunks + c], a);
 #pragma unroll
             for (int j = 0; j < KM; ++j) {
@@ -180,11 +207,11 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(
                 const int64_t at = static_cast<int64_t>(pos[j]) * chunks + c;
                 if (dgates != nullptr) {
                     float b[V];
-                    C::unpack(y_perm[at], b);
+                    C::unpack(y[j], b);
 #pragma unroll
                     for (int i = 0; i < V; ++i) dot[j] = fmaf(a[i], b[i], dot[j]);
                 }
-                if (dy_perm != nullptr) dy_perm[at] = C::scaled(a, g[j]);
+                if (dy_perm != nullptr) store_nt(dy_perm + at, C::scaled(a, g[j]));
             }
         }
         if (dgates == nullptr) continue;
@@ -209,9 +236,14 @@ hipError_t start_combine_backward(const moe_problem_t& p, const void* dy, const 
     using Raw = typename Chunk<T, V>::Raw;
     const unsigned grid = static_cast<unsigned>(p.T);
     const int n = static_cast<int>(p.T * p.k);
-    combine_backward_kernel<T, V, 4><<<grid, 256, 0, s>>>(static_cast<const Raw*>(dy), static_cast<const Raw*>(y_perm),
-                                                          assign_pos, gates, p.k, n, p.d / V,
-                                                          static_cast<Raw*>(dy_perm), dgates);
+    auto start = [&](auto km) {
+        combine_backward_kernel<T, V, decltype(km)::value><<<grid, 256, 0, s>>>(
+            static_cast<const Raw*>(dy), static_cast<const Raw*>(y_perm), assign_pos, gates, p.k, n, p.d / V,
+            static_cast<Raw*>(dy_perm), dgates);
+    };
+    if (p.k <= 2) start(std::integral_constant<int, 2>{});
+    else if (p.k <= 4) start(std::integral_constant<int, 4>{});
+    else start(std::integral_constant<int, 8>{});
     return hipGetLastError();
 }
 
