@@ -17,8 +17,32 @@ namespace moe {
 
 namespace {
 
-// 8 values per lane, 4 lanes per block; consecutive lanes hold consecutive values of
-// the matrix, a workgroup 2048 of them.
+// 8 values (a word of codes) per lane, 4 lanes per block; consecutive lanes hold
+// consecutive words of the matrix.  A workgroup has NW * 256 words, NW of them in flight
+// per lane; which row they lie in follows from one division per workgroup and a short one
+// per word.
+struct At {
+    int64_t word, row;
+    int col;  // of words
+};
+template <int NW>
+__device__ __forceinline__ int64_t first_word() { return static_cast<int64_t>(blockIdx.x) * (NW * 256); }
+
+// words per row below 2^17: the quotient in floats is off by one at most
+__device__ __forceinline__ At place(int64_t first, int64_t row0, int col0, int words, float inv, int i) {
+    const int x = col0 + i;
+    int q = static_cast<int>(static_cast<float>(x) * inv);
+    int r = x - q * words;
+    if (r < 0) {
+        --q;
+        r += words;
+    } else if (r >= words) {
+        ++q;
+        r -= words;
+    }
+    return At{first + i, row0 + q, r};
+}
+
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, float (&v)[8]);
 template <>
@@ -39,96 +63,142 @@ __device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
     for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
 }
 
-template <typename T>
+template <typename T, int NW>
 __global__ __launch_bounds__(256) void quant_rows_mxfp4_kernel(const T* __restrict__ src, int64_t rows, int cols,
                                                               uint32_t* __restrict__ codes,
                                                               uint8_t* __restrict__ scales) {
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;  // words of 8 values
-    const int words = cols / 8;
-    if (at >= rows * words) return;  // (whole blocks leave together)
-    const int64_t r = at / words;
-    const int c = static_cast<int>(at - r * words);
-    float v[8];
-    load8(src + at * 8, v);
-    uint32_t m = 0;
+    const int words = cols / 8, blocks = cols / 32;
+    const int64_t first = first_word<NW>(), all = rows * words;
+    const int64_t row0 = first / words;
+    const int col0 = static_cast<int>(first - row0 * words);
+    const float inv = 1.f / static_cast<float>(words);
+    float v[NW][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-    m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 1, 64)));
-    m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 2, 64)));
-    const bool finite = m < 0x7f800000u;
-    const int byte = finite ? (m == 0 ? 127 : max(static_cast<int>(m >> 23) - 2, 0)) : 255;
-    uint32_t out = 0;
+    for (int n = 0; n < NW; ++n) {
+        const int64_t at = first + n * 256 + threadIdx.x;
+        if (at < all) {  // (whole blocks are in or out)
+            load8(src + at * 8, v[n]);
+        } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        v[i] = fminf(fmaxf(__builtin_amdgcn_ldexpf(v[i], 127 - byte), -6.f), 6.f);
-    out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[0], v[1], 1.f, 0);
-    out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[2], v[3], 1.f, 1);
-    out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[4], v[5], 1.f, 2);
-    out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[6], v[7], 1.f, 3);
-    codes[at] = finite ? out : 0u;
-    if ((c & 3) == 0) {
-        const int b = c / 4, blocks = cols / 32;
-        uint8_t* const dst = scales + static_cast<int64_t>(b / 8) * rows * 8 + r * 8;
-        dst[b & 7] = static_cast<uint8_t>(byte);
-        // the last slice's bytes past the row
-        if (b == blocks - 1)
-            for (int i = (b & 7) + 1; i < 8; ++i) dst[i] = 127;
+            for (int i = 0; i < 8; ++i) v[n][i] = 0.f;
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NW; ++n) {
+        const At at = place(first, row0, col0, words, inv, n * 256 + threadIdx.x);
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[n][i]) & 0x7fffffffu);
+        m = max(m, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(m), 0xB1, 0xf, 0xf, true)));
+        m = max(m, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(m), 0x4E, 0xf, 0xf, true)));
+        const bool finite = m < 0x7f800000u;
+        const int byte = finite ? (m == 0 ? 127 : max(static_cast<int>(m >> 23) - 2, 0)) : 255;
+        float q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            q[i] = __builtin_amdgcn_fmed3f(__builtin_amdgcn_ldexpf(v[n][i], 127 - byte), -6.f, 6.f);
+        uint32_t out = 0;
+        out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, q[0], q[1], 1.f, 0);
+        out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, q[2], q[3], 1.f, 1);
+        out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, q[4], q[5], 1.f, 2);
+        out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, q[6], q[7], 1.f, 3);
+        if (at.word >= all) continue;
+        codes[at.word] = finite ? out : 0u;
+        if ((at.col & 3) == 0) {
+            const int b = at.col / 4;
+            uint8_t* const dst = scales + (static_cast<int64_t>(b / 8) * rows + at.row) * 8;
+            dst[b & 7] = static_cast<uint8_t>(byte);
+            // the last slice's bytes past the row
+            if (b == blocks - 1)
+                for (int i = (b & 7) + 1; i < 8; ++i) dst[i] = 127;
+        }
     }
 }
 
-template <typename O>
+template <typename O, int NW>
 __global__ __launch_bounds__(256) void dequant_rows_mxfp4_kernel(const uint32_t* __restrict__ codes,
                                                                 const uint8_t* __restrict__ scales, int64_t rows,
                                                                 int cols, O* __restrict__ dst) {
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    typedef float f32x2_t __attribute__((ext_vector_type(2)));
     const int words = cols / 8;
-    if (at >= rows * words) return;
-    const int64_t r = at / words;
-    const int b = static_cast<int>(at - r * words) / 4;
-    const int byte = scales[static_cast<int64_t>(b / 8) * rows * 8 + r * 8 + (b & 7)];
-    const uint32_t w = codes[at];
-    float v[8];
+    const int64_t first = first_word<NW>(), all = rows * words;
+    const int64_t row0 = first / words;
+    const int col0 = static_cast<int>(first - row0 * words);
+    const float inv = 1.f / static_cast<float>(words);
+    uint32_t w[NW];
+    int byte[NW];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t code = w >> (4 * i) & 15u, e = code >> 1 & 3u, odd = code & 1u;
-        // 0 or 0.5 below exponent 1, else (1 + odd / 2) 2^(e - 1)
-        const float f = e == 0 ? 0.5f * odd : __builtin_amdgcn_ldexpf(1.f + 0.5f * odd, static_cast<int>(e) - 1);
-        const float x = __builtin_amdgcn_ldexpf(code & 8u ? -f : f, byte - 127);
-        v[i] = byte == 255 ? __uint_as_float(0x7fc00000u) : x;
+    for (int n = 0; n < NW; ++n) {
+        const At at = place(first, row0, col0, words, inv, n * 256 + threadIdx.x);
+        w[n] = 0;
+        byte[n] = 127;
+        if (at.word < all) {
+            const int b = at.col / 4;
+            w[n] = load_nt(codes + at.word);
+            byte[n] = scales[(static_cast<int64_t>(b / 8) * rows + at.row) * 8 + (b & 7)];
+        }
     }
-    if constexpr (sizeof(O) == 4) {
-        float4* const out = reinterpret_cast<float4*>(dst + at * 8);
-        out[0] = make_float4(v[0], v[1], v[2], v[3]);
-        out[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-        *reinterpret_cast<uint4*>(dst + at * 8) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                             pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+#pragma unroll
+    for (int n = 0; n < NW; ++n) {
+        const int64_t at = first + n * 256 + threadIdx.x;
+        if (at >= all) continue;
+        const f32x2_t p[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[n], 1.f, 0),
+                              __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[n], 1.f, 1),
+                              __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[n], 1.f, 2),
+                              __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[n], 1.f, 3)};
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = byte[n] == 255 ? __uint_as_float(0x7fc00000u) : __builtin_amdgcn_ldexpf(p[i / 2][i % 2], byte[n] - 127);
+        if constexpr (sizeof(O) == 4) {
+            float4* const out = reinterpret_cast<float4*>(dst + at * 8);
+            out[0] = make_float4(v[0], v[1], v[2], v[3]);
+            out[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *reinterpret_cast<uint4*>(dst + at * 8) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                                 pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+        }
     }
 }
+
+// Words per lane: one while that leaves workgroups for fewer than four rounds of the CUs.
+bool wide(int64_t words) { return words >= 4 * 4 * 256 * 256; }
 
 }  // namespace
 
 hipError_t launch_quant_rows_mxfp4(const void* src, int64_t rows, int cols, int dtype, void* codes, void* scales,
                                    hipStream_t s) {
-    const unsigned grid = static_cast<unsigned>(ceil_div(rows * (cols / 8), 256));
+    const int64_t words = rows * (cols / 8);
     uint32_t* const c = static_cast<uint32_t*>(codes);
     uint8_t* const sc = static_cast<uint8_t*>(scales);
-    if (dtype == MOE_DTYPE_BF16)
-        quant_rows_mxfp4_kernel<<<grid, 256, 0, s>>>(static_cast<const bf16_t*>(src), rows, cols, c, sc);
-    else
-        quant_rows_mxfp4_kernel<<<grid, 256, 0, s>>>(static_cast<const float*>(src), rows, cols, c, sc);
+    auto start = [&](auto from) {
+        using T = decltype(from);
+        const T* const in = static_cast<const T*>(src);
+        if (wide(words))
+            quant_rows_mxfp4_kernel<T, 4><<<static_cast<unsigned>(ceil_div(words, 1024)), 256, 0, s>>>(in, rows, cols, c, sc);
+        else
+            quant_rows_mxfp4_kernel<T, 1><<<static_cast<unsigned>(ceil_div(words, 256)), 256, 0, s>>>(in, rows, cols, c, sc);
+    };
+    if (dtype == MOE_DTYPE_BF16) start(bf16_t{});
+    else start(float{});
     return hipGetLastError();
 }
 
 hipError_t launch_dequant_rows_mxfp4(const void* codes, const void* scales, int64_t rows, int cols, int dtype,
                                      void* dst, hipStream_t s) {
-    const unsigned grid = static_cast<unsigned>(ceil_div(rows * (cols / 8), 256));
+    const int64_t words = rows * (cols / 8);
     const uint32_t* const c = static_cast<const uint32_t*>(codes);
     const uint8_t* const sc = static_cast<const uint8_t*>(scales);
-    if (dtype == MOE_DTYPE_BF16)
-        dequant_rows_mxfp4_kernel<<<grid, 256, 0, s>>>(c, sc, rows, cols, static_cast<bf16_t*>(dst));
-    else
-        dequant_rows_mxfp4_kernel<<<grid, 256, 0, s>>>(c, sc, rows, cols, static_cast<float*>(dst));
+    auto start = [&](auto to) {
+        using O = decltype(to);
+        O* const out = static_cast<O*>(dst);
+        if (wide(words))
+            dequant_rows_mxfp4_kernel<O, 4><<<static_cast<unsigned>(ceil_div(words, 1024)), 256, 0, s>>>(c, sc, rows, cols, out);
+        else
+            dequant_rows_mxfp4_kernel<O, 1><<<static_cast<unsigned>(ceil_div(words, 256)), 256, 0, s>>>(c, sc, rows, cols, out);
+    };
+    if (dtype == MOE_DTYPE_BF16) start(bf16_t{});
+    else start(float{});
     return hipGetLastError();
 }
 
