@@ -72,11 +72,17 @@ def _launch(device: torch.device, where: str, fn, *args):
     """Calls an entry point of the C ABI with the current stream of ``device``
     as its last argument; ``device`` is current meanwhile (a kernel starts on
     the current device)."""
-    if device.index == torch.cuda.current_device():
+    if device.index == torch._C._cuda_getDevice():
         L.check(fn(*args, torch._C._cuda_getCurrentRawStream(device.index)), where)
     else:
         with torch.cuda.device(device):
             L.check(fn(*args, torch._C._cuda_getCurrentRawStream(device.index)), where)
+
+
+def _on_gpu(device: torch.device):
+    """The tensors that have passed ``_expect`` with this device are on a GPU."""
+    if device.type != "cuda":
+        raise ValueError("tensors must live on the GPU")
 
 
 def _addr(t: Optional[torch.Tensor]):
@@ -149,8 +155,10 @@ def route(k: int, x: Optional[torch.Tensor] = None, w_router: Optional[torch.Ten
 _SCORES = {"softmax": L.MOE_SCORE_SOFTMAX, "sigmoid": L.MOE_SCORE_SIGMOID}
 
 
+@functools.lru_cache(maxsize=4096)
 def _gating(T: int, E: int, k: int, score: str, groups: int, groups_kept: Optional[int], group_top: int,
             renormalise: bool, scale: float, d: int = 1, dtype=torch.float32) -> L.MoeGating:
+    """The ABI struct (shared: not to be written to)."""
     if score not in _SCORES:
         raise ValueError(f"score {score!r}, expected 'softmax' or 'sigmoid'")
     return L.MoeGating(T=T, d=d, dtype=_DTYPES[dtype], E=E, k=k, score=_SCORES[score], groups=groups,
@@ -211,11 +219,14 @@ def route_scored(k: int, x: Optional[torch.Tensor] = None, w_router: Optional[to
         ids = torch.empty((T, k), dtype=torch.int32, device=dev)
     if gates is None:
         gates = torch.empty((T, k), dtype=torch.float32, device=dev)
-    ptrs = (_addr(x), _addr(w_router), _addr(logits), None if logits is not None else _addr(logits_out), _addr(bias),
-            _addr(ids), _addr(gates), _addr(score_sums) if with_score_sums else None,
-            _addr(ws) if with_score_sums else None)
+    _on_gpu(dev)
     if T > 0 or with_score_sums:
-        _launch(dev, "moe_route_scored", L.load().moe_route_scored, ctypes.byref(g), *ptrs, nbytes)
+        given = logits is not None
+        _launch(dev, "moe_route_scored", L.load().moe_route_scored, ctypes.byref(g), None if given else x.data_ptr(),
+                None if given else w_router.data_ptr(), logits.data_ptr() if given else None,
+                None if given else logits_out.data_ptr(), None if bias is None else bias.data_ptr(), ids.data_ptr(),
+                gates.data_ptr(), score_sums.data_ptr() if with_score_sums else None,
+                ws.data_ptr() if with_score_sums else None, nbytes)
     return (ids, gates, logits_out, score_sums) if with_score_sums else (ids, gates, logits_out)
 
 
@@ -250,8 +261,10 @@ def route_scored_backward(logits: torch.Tensor, topk_ids: torch.Tensor, dgates: 
     if dlogits is None:
         dlogits = torch.empty((T, E), dtype=dtype, device=dev)
     g = _gating(T, E, k, score, 1, None, 1, renormalise, scale)
-    ptrs = (_addr(logits), _addr(topk_ids), _addr(dgates), _addr(dscore_sums), _DTYPES[dtype], _addr(dlogits))
-    _launch(dev, "moe_route_scored_backward", L.load().moe_route_scored_backward, ctypes.byref(g), *ptrs)
+    _on_gpu(dev)
+    _launch(dev, "moe_route_scored_backward", L.load().moe_route_scored_backward, ctypes.byref(g), logits.data_ptr(),
+            topk_ids.data_ptr(), dgates.data_ptr(), None if dscore_sums is None else dscore_sums.data_ptr(),
+            _DTYPES[dtype], dlogits.data_ptr())
     return dlogits
 
 
@@ -421,10 +434,11 @@ def combine_backward(dy: torch.Tensor, assign_pos: torch.Tensor, gates: torch.Te
         res["dgates"] = None
     elif res.get("dgates") is None:
         res["dgates"] = torch.empty((T, k), dtype=torch.float32, device=dev)
-    p = problem(T, d, k, k, 64, dt)
-    ptrs = (_addr(dy), _addr(y_perm) if with_dgates else None, _addr(assign_pos), _addr(gates), _addr(res["dy_perm"]),
-            _addr(res["dgates"]))
-    _launch(dev, "moe_combine_backward", L.load().moe_combine_backward, ctypes.byref(p), *ptrs)
+    _on_gpu(dev)
+    p = L.MoeProblem(T, d, k, k, 64, _DTYPES[dt])
+    _launch(dev, "moe_combine_backward", L.load().moe_combine_backward, ctypes.byref(p), dy.data_ptr(),
+            y_perm.data_ptr() if with_dgates else None, assign_pos.data_ptr(), gates.data_ptr(),
+            res["dy_perm"].data_ptr() if with_dy_perm else None, res["dgates"].data_ptr() if with_dgates else None)
     return res
 
 
@@ -821,8 +835,9 @@ def quantize_rows_mxfp4(src: torch.Tensor, codes: Optional[torch.Tensor] = None,
         scales = torch.empty((_mxfp4_slices(cols), rows, 8), dtype=torch.uint8, device=dev)
     else:
         _expect("scales", scales, (_mxfp4_slices(cols), rows, 8), torch.uint8, dev)
-    ptrs = (_addr(src), rows, cols, _DTYPES[dt], _addr(codes), _addr(scales))
-    _launch(dev, "moe_quantize_rows_mxfp4", L.load().moe_quantize_rows_mxfp4, *ptrs)
+    _on_gpu(dev)
+    _launch(dev, "moe_quantize_rows_mxfp4", L.load().moe_quantize_rows_mxfp4, src.data_ptr(), rows, cols, _DTYPES[dt],
+            codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -842,8 +857,9 @@ def dequantize_rows_mxfp4(codes: torch.Tensor, scales: torch.Tensor, dtype=torch
         out = torch.empty((rows, cols), dtype=dtype, device=dev)
     else:
         _expect("out", out, (rows, cols), dtype, dev)
-    ptrs = (_addr(codes), _addr(scales), rows, cols, _DTYPES[dtype], _addr(out))
-    _launch(dev, "moe_dequantize_rows_mxfp4", L.load().moe_dequantize_rows_mxfp4, *ptrs)
+    _on_gpu(dev)
+    _launch(dev, "moe_dequantize_rows_mxfp4", L.load().moe_dequantize_rows_mxfp4, codes.data_ptr(), scales.data_ptr(),
+            rows, cols, _DTYPES[dtype], out.data_ptr())
     return out
 
 
@@ -873,9 +889,11 @@ def grouped_matmul_mxfp4(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tenso
         c = torch.empty((R, N), dtype=out_dtype, device=dev)
     else:
         _expect("c", c, (R, N), out_dtype, dev)
-    g = L.MoeGrouped(rows=R, E=E, N=N, K=2 * half, dtype=_DTYPES[out_dtype])
-    ptrs = (_addr(a), _addr(a_scales), _addr(w), _addr(w_scales), _addr(offsets), _addr(c))
-    _launch(dev, "moe_grouped_matmul_mxfp4", L.load().moe_grouped_matmul_mxfp4, ctypes.byref(g), *ptrs)
+    _on_gpu(dev)
+    g = L.MoeGrouped(R, E, N, 2 * half, _DTYPES[out_dtype])
+    _launch(dev, "moe_grouped_matmul_mxfp4", L.load().moe_grouped_matmul_mxfp4, ctypes.byref(g), a.data_ptr(),
+            a_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(), None if offsets is None else offsets.data_ptr(),
+            c.data_ptr())
     return c
 
 

@@ -60,28 +60,21 @@ __device__ __forceinline__ double key_min(double a, double b) {
     asm("v_min_f64 %0, %1, %2" : "=v"(d) : "v"(a), "v"(b));
     return d;
 }
-__device__ __forceinline__ uint32_t key_low(bool negative, int e) { return static_cast<uint32_t>(negative ? e : 255 - e); }
+__device__ __forceinline__ double key_of(uint32_t hi, int e) {
+    const uint32_t sign = static_cast<uint32_t>(static_cast<int32_t>(hi) >> 31);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | (sign ^ static_cast<uint32_t>(255 - e)));
+}
 __device__ __forceinline__ int key_index(double key) {
     const uint64_t b = __builtin_bit_cast(uint64_t, key);
-    const int low = static_cast<int>(b & 255u);
-    return b >> 63 ? low : 255 - low;
+    return 255 - static_cast<int>(static_cast<uint32_t>(b) ^ static_cast<uint32_t>(static_cast<int64_t>(b) >> 63));
 }
-
-// An expert that is out: below every c.
-__device__ __forceinline__ double out_key(int e) {
-    return __builtin_bit_cast(double, 0xffefffff00000000ull | static_cast<uint32_t>(e));
-}
-
-// c in 32 bits: its bits are the upper half.  (Any float's are those of a finite
-// 64-bit one, minus infinity's of one above out_key.)
-__device__ __forceinline__ double key32(float c, int e) {
-    c = c == c ? c + 0.f : -INFINITY;  // (a NaN comes last; -0 is 0)
-    const uint32_t hi = __float_as_uint(c);
-    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | key_low(hi >> 31, e));
-}
-__device__ __forceinline__ float key32_value(double key) {
+__device__ __forceinline__ float key_value(double key) {
     return __uint_as_float(static_cast<uint32_t>(__builtin_bit_cast(uint64_t, key) >> 32));
 }
+// Upper halves: of c (any float's bits are those of a finite 64-bit one; a NaN comes
+// last, -0 is 0), and of what is out, below minus infinity.
+__device__ __forceinline__ uint32_t key_high(float c) { return __float_as_uint(fmaxf(c + 0.f, -INFINITY)); }
+constexpr uint32_t kOut = 0xffefffffu;
 
 // ---- within the G lanes of a token ---------------------------------------------------
 //
@@ -113,14 +106,15 @@ __device__ __forceinline__ int turned(int v) {
         return __builtin_amdgcn_update_dpp(0, v, I | ((1 + I) & 3) << 2 | ((2 + I) & 3) << 4 | ((3 + I) & 3) << 6, 0xf, 0xf, true);
     else return __shfl(v, (lane_id() & ~(G - 1)) | ((lane_id() + I) & (G - 1)), 64);
 }
-// How many of the token's other lanes have a larger key.
-template <int G, int I = 1>
+// How many of the token's other lanes (every STEP-th) have a larger key.
+template <int G, int STEP, int I = STEP>
 __device__ __forceinline__ int larger_keys(double key) {
-    if constexpr (I == G) return 0;
+    if constexpr (I >= G) return 0;
     else {
         const uint64_t b = __builtin_bit_cast(uint64_t, key);
         const uint32_t lo = turned<G, I>(static_cast<int>(b)), hi = turned<G, I>(static_cast<int>(b >> 32));
-        return (__builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo) > key ? 1 : 0) + larger_keys<G, I + 1>(key);
+        return (__builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo) > key ? 1 : 0) +
+               larger_keys<G, STEP, I + STEP>(key);
     }
 }
 template <int G, typename T, typename F>
@@ -132,12 +126,10 @@ __device__ __forceinline__ T reduce(T v, F op) {
     return v;
 }
 struct Max {
-    template <typename T>
-    __device__ __forceinline__ T operator()(T a, T b) const { return a > b ? a : b; }
+    __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
 };
 struct Min {
-    template <typename T>
-    __device__ __forceinline__ T operator()(T a, T b) const { return a < b ? a : b; }
+    __device__ __forceinline__ float operator()(float a, float b) const { return fminf(a, b); }
 };
 struct Add {
     template <typename T>
@@ -329,19 +321,21 @@ __global__ __launch_bounds__(256) void route_scored_wave_kernel(moe_gating_t g, 
 // power of two of them) are valued by the heads of the lists, and the lists of groups that
 // go are dropped; other groups are valued from LDS before the lists are made.
 //
-// Errors: exp2 of the rounded product l log2(e), and the reciprocal, leave s with an
-// absolute error below 2^-21 max s (s |l| and s |l - max| are below 1 / e of it; the
-// softmax's sum adds 20 roundings to all of a token's s alike, which with a bias counts as
-// 2^-19.6 max s), the sum with the bias below 2^-24 |c|.  A choice is taken for certain if
-// all that it compared differs by more than 2^-18 max s + 2^-21 max |c| (twice that for
-// sums of two), else made again in 64 bits.
+// Errors, u = 2^-24.  Sigmoid: exp2 of the rounded product l log2(e) is off by (|l| + 2) u
+// of itself, which counts s (1 - s) times in s, and |l| s (1 - s) < 1 / 4; the sum and the
+// reciprocal add 3 u s: together below 4 u, 8 u for a difference of two.  Softmax: (2 |l - max|
+// + 2) u of s, where |l - max| s < max s, and the quotient 1 u; its sum's error, 24 u, is the
+// same share of all of a token's s, so it counts once in a difference: 24 u + 2 * 5 u of max s,
+// below 2^-18.9.  The sum with the bias adds 2 u |c| to a difference.  A choice is taken for
+// certain if all that it compared differs by more than 2^-20 (softmax: 2^-18 max s) + 2^-22
+// max |c|, twice that for groups (sums of two), else it is made again in 64 bits.
 //
 // 32768 tokens, 256 experts: see the launch below.
 constexpr int kMaxRounds = 32;  // of tokens that a workgroup takes one after the other
 constexpr float kLog2e = 1.44269504088896340736f;
 
 template <int G, int EPL, bool VEC>
-__global__ __launch_bounds__(256, 3) void route_scored_kernel(moe_gating_t g, const float* __restrict__ logits,
+__global__ __launch_bounds__(256, EPL == 16 && !VEC ? 3 : 4) void route_scored_kernel(moe_gating_t g, const float* __restrict__ logits,
                                                           const float* __restrict__ bias, int32_t* __restrict__ ids,
                                                           float* __restrict__ gates, float* __restrict__ partial) {
     constexpr int TPW = 64 / G;              // tokens per wave
@@ -371,12 +365,29 @@ __global__ __launch_bounds__(256, 3) void route_scored_kernel(moe_gating_t g, co
         // (lanes past the last token work on it once more and store nothing)
         const int64_t t = has ? t0 + row : g.T - 1;
         const float* const from = logits + t * E;
-        float c[EPL], s[EPL];
+        float c[EPL], s[EPL], b[EPL];
+        if (bias != nullptr) {
+#pragma unroll
+            for (int i = 0; i < EPL; i += VEC ? 4 : 1) {
+                if constexpr (VEC) {
+                    const float4 v = *reinterpret_cast<const float4*>(bias + min(e0 + i, E - 4));
+                    b[i] = v.x;
+                    b[i + 1] = v.y;
+                    b[i + 2] = v.z;
+                    b[i + 3] = v.w;
+                } else {
+                    b[i] = bias[min(e0 + i, E - 1)];
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) b[i] = 0.f;
+        }
+        // (experts past the last: minus infinity, read from the row's end)
         if constexpr (VEC) {
 #pragma unroll
             for (int i = 0; i < EPL; i += 4) {
-                const float4 v = e0 + i < E ? *reinterpret_cast<const float4*>(from + e0 + i)
-                                            : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                const float4 v = *reinterpret_cast<const float4*>(from + min(e0 + i, E - 4));
                 c[i] = v.x;
                 c[i + 1] = v.y;
                 c[i + 2] = v.z;
@@ -384,10 +395,16 @@ __global__ __launch_bounds__(256, 3) void route_scored_kernel(moe_gating_t g, co
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) c[i] = e0 + i < E ? from[e0 + i] : -INFINITY;
+            for (int i = 0; i < EPL; ++i) c[i] = from[min(e0 + i, E - 1)];
+        }
+        uint32_t gone = ~0u << min(max(E - e0, 0), EPL);  // bit i: expert e0 + i is out
+        asm volatile("" : "+v"(gone));       // (keeps masks made of it out of scalar registers)
+        if (e0 + EPL > E) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) c[i] = gone >> i & 1 ? -INFINITY : c[i];
         }
         // scores (experts past the last: zero)
-        float top = -INFINITY, inv = 1.f, s_max = 1.f;
+        float top = -INFINITY, inv = 1.f, s_error = 0x1p-20f;
         if (g.score == MOE_SCORE_SOFTMAX) {
 #pragma unroll
             for (int i = 0; i < EPL; ++i) top = fmaxf(top, c[i]);
@@ -401,7 +418,7 @@ __global__ __launch_bounds__(256, 3) void route_scored_kernel(moe_gating_t g, co
             }
             z = reduce<G>(z, Add());
             inv = z == 0.f ? 0.f : 1.f / z;
-            s_max = inv;
+            s_error = 0x1p-18f * inv;  // (the largest s is 1 / z)
 #pragma unroll
             for (int i = 0; i < EPL; ++i) s[i] *= inv;
         } else {
@@ -414,13 +431,10 @@ __global__ __launch_bounds__(256, 3) void route_scored_kernel(moe_gating_t g, co
         }
         if (!by_logit) {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) c[i] = s[i] + (bias != nullptr && e0 + i < E ? bias[e0 + i] : 0.f);
+            for (int i = 0; i < EPL; ++i) c[i] = s[i] + b[i];
         }
         bool sure = true;
         bool dropped = false;                // the lane's experts are out
-        uint32_t gone = 0;                   // bit i: expert e0 + i is out
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) gone |= (e0 + i < E ? 0u : 1u) << i;
         float* const c_of = reinterpret_cast<float*>(s_buf[wave]) + row * EMAX;
         float* const v_of = reinterpret_cast<float*>(s_buf[wave]) + TPW * EMAX + row * EMAX;
         // the groups that stay differ from those that go by more than the error
@@ -428,7 +442,7 @@ __global__ __launch_bounds__(256, 3) void route_scored_kernel(moe_gating_t g, co
             low = reduce<G>(low, Min());
             high = reduce<G>(high, Max());
             most = reduce<G>(most, Max());
-            return low - high > 2.f * (0x1p-18f * s_max + 0x1p-21f * most);
+            return low - high > 2.f * (s_error + 0x1p-22f * most);
         };
         if (limited && !whole_lanes) {
 #pragma unroll
@@ -469,7 +483,7 @@ __global__ __launch_bounds__(256, 3) void route_scored_kernel(moe_gating_t g, co
             int q = e0 / size, r = e0 - q * size;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
-                if (e0 + i < E && v_of[q] == 0.f) gone |= 1u << i;
+                if (v_of[min(q, g.groups - 1)] == 0.f) gone |= 1u << i;
                 if (++r == size) {
                     r = 0;
                     ++q;
@@ -480,7 +494,7 @@ __global__ __launch_bounds__(256, 3) void route_scored_kernel(moe_gating_t g, co
         }
         double list[EPL];
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) list[i] = gone >> i & 1 ? out_key(e0 + i) : key32(c[i], e0 + i);
+        for (int i = 0; i < EPL; ++i) list[i] = key_of(gone >> i & 1 ? kOut : key_high(c[i]), e0 + i);
         sort8(list);
         if constexpr (EPL == 16) {
             sort8(list + 8);
@@ -489,7 +503,7 @@ __global__ __launch_bounds__(256, 3) void route_scored_kernel(moe_gating_t g, co
         if (whole_lanes) {
             // the group's two largest, from the lists' heads
             const bool live = e0 < E;
-            float a = live ? key32_value(list[0]) : -INFINITY, a2 = live ? key32_value(list[1]) : -INFINITY;
+            float a = live ? key_value(list[0]) : -INFINITY, a2 = live ? key_value(list[1]) : -INFINITY;
             auto join = [&](float p, float p2) {
                 a2 = fmaxf(fminf(a, p), fmaxf(a2, p2));
                 a = fmaxf(a, p);
@@ -502,15 +516,16 @@ __global__ __launch_bounds__(256, 3) void route_scored_kernel(moe_gating_t g, co
             float v = g.group_top == 2 ? a + a2 : a;
             // (the group's number, counted from the token's first lane)
             const int q = s_lane / per_group;
-            const double mine = live ? key32(v, q) : out_key(q);
-            v = key32_value(key32(v, q));
-            const int better = larger_keys<G>(mine);
+            v = __uint_as_float(key_high(v));
+            const double mine = key_of(live ? __float_as_uint(v) : kOut, q);
+            // (lanes of groups that come before; every other lane where a group has two)
+            const int better = per_group == 1 ? larger_keys<G, 1>(mine) : 2 * larger_keys<G, 2>(mine);
             dropped = better >= g.groups_kept * per_group;
             if (!by_logit)
                 sure = apart(live && !dropped ? v : INFINITY, live && dropped ? v : -INFINITY,
                              live ? fmaxf(fabsf(a), fabsf(a2)) : 0.f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) list[i] = dropped ? out_key(e0 + i) : list[i];
+            for (int i = 0; i < 8; ++i) list[i] = dropped ? key_of(kOut, e0 + i) : list[i];
         }
         merge_partner<0>(list);
         merge_partner<1>(list);
@@ -522,7 +537,7 @@ __global__ __launch_bounds__(256, 3) void route_scored_kernel(moe_gating_t g, co
             float gap = INFINITY;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float v = key32_value(list[j]);
+                const float v = key_value(list[j]);
                 if (j < k) {
                     if (j > 0) gap = fminf(gap, last - v);
                     most = fmaxf(most, fabsf(v));
@@ -530,7 +545,7 @@ __global__ __launch_bounds__(256, 3) void route_scored_kernel(moe_gating_t g, co
                     last = v;
                 }
             }
-            const float tol = 0x1p-18f * s_max + 0x1p-21f * most;
+            const float tol = s_error + 0x1p-22f * most;
             // no others within the error of the last
             int near = 0;
 #pragma unroll
@@ -601,23 +616,27 @@ __global__ __launch_bounds__(256, 3) void route_scored_kernel(moe_gating_t g, co
     }
 }
 
-// sums[e] = the sum of the blocks' partial sums, in a fixed order: 32 experts per
-// workgroup, 8 threads each.
-__global__ __launch_bounds__(256) void score_sums_kernel(const float* __restrict__ partial, int64_t blocks, int E,
-                                                        float* __restrict__ sums) {
-    __shared__ double s[8][33];
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int e = blockIdx.x * 32 + x;
+// sums[e] = the sum of the blocks' partial sums, in a fixed order: 8 experts per
+// workgroup, 128 threads each, so that up to 1024 blocks' are one load per lane in
+// flight eight times.
+__global__ __launch_bounds__(1024) void score_sums_kernel(const float* __restrict__ partial, int64_t blocks, int E,
+                                                         float* __restrict__ sums) {
+    __shared__ double s[16][8];
+    const int x = threadIdx.x & 7, y = threadIdx.x >> 3;
+    const int e = blockIdx.x * 8 + x;
     double v = 0;
     if (e < E) {
 #pragma unroll 8
-        for (int64_t b = y; b < blocks; b += 8) v += partial[b * E + e];
+        for (int64_t b = y; b < blocks; b += 128) v += partial[b * E + e];
     }
-    s[y][x] = v;
-    __syncthreads();
-    if (y == 0 && e < E) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) v += s[i][x];
+    for (int off = 8; off < 64; off <<= 1) v += __shfl_xor(v, off, 64);
+    if ((threadIdx.x & 63) < 8) s[threadIdx.x >> 6][x] = v;
+    __syncthreads();
+    if (threadIdx.x < 8 && e < E) {
+        v = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v += s[i][x];
         sums[e] = static_cast<float>(v);
     }
 }
@@ -812,12 +831,12 @@ int lanes_for(int E) { return E <= 32 ? 4 : (E <= 64 ? 8 : 16); }
 
 }  // namespace
 
-// Workgroups: one round of tokens each up to 512 of them, then up to kMaxRounds
+// Workgroups: one round of tokens each up to 1024 of them, then up to kMaxRounds
 // (each lane adds that many scores in 32 bits).
 int64_t route_scored_blocks(const moe_gating_t& g) {
     const int64_t per_round = g.k <= 8 ? 4 * (64 / lanes_for(g.E)) : 4;
     const int64_t rounds = ceil_div(g.T, per_round);
-    return std::max(std::min<int64_t>(rounds, 512), ceil_div(rounds, kMaxRounds));
+    return std::max(std::min<int64_t>(rounds, 1024), ceil_div(rounds, kMaxRounds));
 }
 
 hipError_t launch_route_scored(const moe_gating_t& g, const float* logits, const float* bias, int32_t* ids,
@@ -841,7 +860,7 @@ hipError_t launch_route_scored(const moe_gating_t& g, const float* logits, const
 #undef MOE_ROUTE
     }
     if (score_sums != nullptr)
-        score_sums_kernel<<<static_cast<unsigned>(ceil_div(g.E, 32)), 256, 0, s>>>(partial, blocks, g.E, score_sums);
+        score_sums_kernel<<<static_cast<unsigned>(ceil_div(g.E, 8)), 1024, 0, s>>>(partial, blocks, g.E, score_sums);
     return hipGetLastError();
 }
 
