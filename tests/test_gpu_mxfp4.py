@@ -60,6 +60,16 @@ def test_quantise(rows, cols, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(4099, 2080), (8192, 1024), (131, 65504)])
+def test_quantise_large(rows, cols, dtype):
+    """Enough for a slice of rows per workgroup; rows and columns that end inside one."""
+    x = normal(rows, rows, cols, dtype=dtype)
+    x[rows - 1, cols - 5], x[7, 300] = np.nan, np.inf
+    x[11, 320:352] = 0
+    check_quantise(x)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_quantise_borders(dtype):
     """Every rounding border and its neighbours, at every scale of the type."""
     base = np.array([0, 0.25, 0.5, 0.75, 1, 1.25, 1.5, 1.75, 2, 2.5, 3, 3.5, 4, 5, 6, 7], np.float32)
