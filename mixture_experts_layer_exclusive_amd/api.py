@@ -158,7 +158,7 @@ _SCORES = {"softmax": L.MOE_SCORE_SOFTMAX, "sigmoid": L.MOE_SCORE_SIGMOID}
 @functools.lru_cache(maxsize=4096)
 def _gating(T: int, E: int, k: int, score: str, groups: int, groups_kept: Optional[int], group_top: int,
             renormalise: bool, scale: float, d: int = 1, dtype=torch.float32) -> L.MoeGating:
-    """The ABI struct (shared: not to be written to)."""
+    """The ABI struct (shared by calls alike: not to be written to)."""
     if score not in _SCORES:
         raise ValueError(f"score {score!r}, expected 'softmax' or 'sigmoid'")
     return L.MoeGating(T=T, d=d, dtype=_DTYPES[dtype], E=E, k=k, score=_SCORES[score], groups=groups,
@@ -207,13 +207,13 @@ def route_scored(k: int, x: Optional[torch.Tensor] = None, w_router: Optional[to
     _expect("gates", gates, (T, k), torch.float32, dev, required=False)
     _expect("score_sums", score_sums, (E,), torch.float32, dev, required=False)
     _expect_ws(ws, dev)
-    g = _gating(T, E, k, score, groups, groups_kept, group_top, renormalise, scale, d, dt)
+    g = _gating(T, E, k, score, int(groups), groups_kept, int(group_top), bool(renormalise), float(scale), d, dt)
     nbytes = 0
     if with_score_sums:
         if score_sums is None:
             score_sums = torch.empty((E,), dtype=torch.float32, device=dev)
         if ws is None:
-            ws = torch.empty((max(route_scored_workspace_size(g), 256),), dtype=torch.uint8, device=dev)
+            ws = torch.empty((max(route_scored_workspace_size(T, E, k), 256),), dtype=torch.uint8, device=dev)
         nbytes = ws.numel() * ws.element_size()
     if ids is None:
         ids = torch.empty((T, k), dtype=torch.int32, device=dev)
@@ -230,8 +230,10 @@ def route_scored(k: int, x: Optional[torch.Tensor] = None, w_router: Optional[to
     return (ids, gates, logits_out, score_sums) if with_score_sums else (ids, gates, logits_out)
 
 
-def route_scored_workspace_size(g: L.MoeGating) -> int:
+@functools.lru_cache(maxsize=4096)
+def route_scored_workspace_size(T: int, E: int, k: int) -> int:
     """Workspace bytes of ``route_scored`` with score sums."""
+    g = _gating(T, E, k, "softmax", 1, None, 1, True, 1.0)
     n = ctypes.c_size_t(0)
     L.check(L.load().moe_route_scored_workspace_size(ctypes.byref(g), ctypes.byref(n)),
             "moe_route_scored_workspace_size")
@@ -260,7 +262,7 @@ def route_scored_backward(logits: torch.Tensor, topk_ids: torch.Tensor, dgates: 
     _expect("dlogits", dlogits, (T, E), dtype, dev, required=False)
     if dlogits is None:
         dlogits = torch.empty((T, E), dtype=dtype, device=dev)
-    g = _gating(T, E, k, score, 1, None, 1, renormalise, scale)
+    g = _gating(T, E, k, score, 1, None, 1, bool(renormalise), float(scale))
     _on_gpu(dev)
     _launch(dev, "moe_route_scored_backward", L.load().moe_route_scored_backward, ctypes.byref(g), logits.data_ptr(),
             topk_ids.data_ptr(), dgates.data_ptr(), None if dscore_sums is None else dscore_sums.data_ptr(),

@@ -10,7 +10,7 @@
 // the 30th bit are in the right order.  Without a bias c has the order of the
 // logits, which then stand for it (unless groups are valued by sums).
 //
-// For k <= 8 the choice is made in 32 bits by G lanes per token, and where it hangs
+// For k <= 16 the choice is made in 32 bits by G lanes per token, and where it hangs
 // on a difference that 32 bits may have got wrong (about one token in 300), the whole
 // wave makes that token's choice again in 64 bits.
 #include <float.h>
@@ -136,39 +136,76 @@ struct Add {
     __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
 };
 
-// ---- sorted lists of 8 keys, the largest first -------------------------------------
+// ---- sorted lists of KM keys, the largest first ---------------------------------------
 
 __device__ __forceinline__ void order(double& a, double& b) {
     const double x = key_max(a, b);
     b = key_min(a, b);
     a = x;
 }
-// (the 19 comparisons of Batcher's odd-even merge sort)
+__device__ __forceinline__ void sort4(double* v) {
+    order(v[0], v[1]); order(v[2], v[3]);
+    order(v[0], v[2]); order(v[1], v[3]);
+    order(v[1], v[2]);
+}
+// (19 comparisons: Batcher's odd-even merge sort)
 __device__ __forceinline__ void sort8(double* v) {
-    order(v[0], v[1]); order(v[2], v[3]); order(v[4], v[5]); order(v[6], v[7]);
-    order(v[0], v[2]); order(v[1], v[3]); order(v[4], v[6]); order(v[5], v[7]);
-    order(v[1], v[2]); order(v[5], v[6]);
+    sort4(v);
+    sort4(v + 4);
     order(v[0], v[4]); order(v[1], v[5]); order(v[2], v[6]); order(v[3], v[7]);
     order(v[2], v[4]); order(v[3], v[5]);
     order(v[1], v[2]); order(v[3], v[4]); order(v[5], v[6]);
 }
-// The 8 largest of a and b (b the other way round: the larger of each pair are they,
-// first rising and then falling), sorted.
-__device__ __forceinline__ void merge8(double* a, const double* b) {
+// Sorts keys that first rise and then fall, or the other way.
+template <int KM>
+__device__ __forceinline__ void straighten(double* a) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = key_max(a[i], b[7 - i]);
+    for (int d = KM / 2; d > 0; d >>= 1)
 #pragma unroll
-    for (int d = 4; d > 0; d >>= 1)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < KM; ++i)
             if ((i & d) == 0) order(a[i], a[i + d]);
 }
-template <int STEP>
-__device__ __forceinline__ void merge_partner(double* a) {
-    double b[8];
+// The KM largest of a and b, sorted: with b the other way round the larger of each pair
+// are they.
+template <int KM>
+__device__ __forceinline__ void merge(double* a, const double* b) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = partner<STEP>(a[i]);
-    merge8(a, b);
+    for (int i = 0; i < KM; ++i) a[i] = key_max(a[i], b[KM - 1 - i]);
+    straighten<KM>(a);
+}
+template <int STEP, int KM>
+__device__ __forceinline__ void merge_partner(double* a) {
+    double b[KM];
+#pragma unroll
+    for (int i = 0; i < KM; ++i) b[i] = partner<STEP>(a[i]);
+    merge<KM>(a, b);
+}
+// A lane's EPL keys: the KM largest of them, sorted (fewer: the list has room after them).
+template <int KM, int EPL>
+__device__ __forceinline__ void sort_lane(double* v) {
+    static_assert(EPL == 8 || EPL == 16, "experts per lane");
+    if constexpr (KM == 4) {
+#pragma unroll
+        for (int i = 0; i < EPL; i += 4) sort4(v + i);
+#pragma unroll
+        for (int i = 4; i < EPL; i += 4) merge<4>(v, v + i);
+    } else {
+        sort8(v);
+        if constexpr (EPL == 16) {
+            sort8(v + 8);
+            if constexpr (KM == 8) {
+                merge<8>(v, v + 8);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const double x = v[8 + i];
+                    v[8 + i] = v[15 - i];
+                    v[15 - i] = x;
+                }
+                straighten<16>(v);
+            }
+        }
+    }
 }
 
 // ---- a token's choice in 64 bits, by a whole wave ---------------------------------------
@@ -316,7 +353,7 @@ __global__ __launch_bounds__(256) void route_scored_wave_kernel(moe_gating_t g, 
 
 // ---- a token's choice in 32 bits, by G lanes ------------------------------------------------
 //
-// Lane s of a token has the EPL experts from EPL * s on.  Each lane sorts its 8
+// Lane s of a token has the EPL experts from EPL * s on.  Each lane sorts its KM >= k
 // largest keys, and the lists are merged over the lanes.  Groups that are whole lanes (a
 // power of two of them) are valued by the heads of the lists, and the lists of groups that
 // go are dropped; other groups are valued from LDS before the lists are made.
@@ -331,11 +368,39 @@ __global__ __launch_bounds__(256) void route_scored_wave_kernel(moe_gating_t g, 
 // max |c|, twice that for groups (sums of two), else it is made again in 64 bits.
 //
 // 32768 tokens, 256 experts: see the launch below.
+constexpr int kMaxList = 16;    // the longest list: larger k go to the whole wave's choice
 constexpr int kMaxRounds = 32;  // of tokens that a workgroup takes one after the other
 constexpr float kLog2e = 1.44269504088896340736f;
 
-template <int G, int EPL, bool VEC>
-__global__ __launch_bounds__(256, EPL == 16 && !VEC ? 3 : 4) void route_scored_kernel(moe_gating_t g, const float* __restrict__ logits,
+typedef float f32x4_any_t __attribute__((ext_vector_type(4), aligned(4)));
+
+// Values e0 .. e0 + EPL - 1 of a row of E >= 4, in 16-byte loads whatever the row's
+// alignment (4-byte loads: 250 experts 48 us for 36).  The last load of a row ends with it;
+// unless E is a multiple of 4 (VEC), what it holds is moved down.  Values past the row are
+// any.
+template <int EPL, bool VEC>
+__device__ __forceinline__ void load_experts(const float* __restrict__ row, int e0, int E, float (&v)[EPL]) {
+#pragma unroll
+    for (int i = 0; i < EPL; i += 4) {
+        const f32x4_any_t w = *reinterpret_cast<const f32x4_any_t*>(row + min(e0 + i, E - 4));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i + j] = w[j];
+    }
+    if (!VEC && e0 + EPL > E) {
+#pragma unroll
+        for (int i = 0; i < EPL; i += 4) {
+            const int by = e0 + i - (E - 4);  // 1, 2, 3: the row ends in this load
+            if (by > 0 && by < 4) {
+                v[i] = by == 1 ? v[i + 1] : (by == 2 ? v[i + 2] : v[i + 3]);
+                v[i + 1] = by == 1 ? v[i + 2] : v[i + 3];
+                v[i + 2] = v[i + 3];
+            }
+        }
+    }
+}
+
+template <int G, int EPL, bool VEC, int KM>
+__global__ __launch_bounds__(256, KM == 16 || (EPL == 16 && !VEC) ? 3 : 4) void route_scored_kernel(moe_gating_t g, const float* __restrict__ logits,
                                                           const float* __restrict__ bias, int32_t* __restrict__ ids,
                                                           float* __restrict__ gates, float* __restrict__ partial) {
     constexpr int TPW = 64 / G;              // tokens per wave
@@ -365,40 +430,11 @@ __global__ __launch_bounds__(256, EPL == 16 && !VEC ? 3 : 4) void route_scored_k
         // (lanes past the last token work on it once more and store nothing)
         const int64_t t = has ? t0 + row : g.T - 1;
         const float* const from = logits + t * E;
-        float c[EPL], s[EPL], b[EPL];
-        if (bias != nullptr) {
-#pragma unroll
-            for (int i = 0; i < EPL; i += VEC ? 4 : 1) {
-                if constexpr (VEC) {
-                    const float4 v = *reinterpret_cast<const float4*>(bias + min(e0 + i, E - 4));
-                    b[i] = v.x;
-                    b[i + 1] = v.y;
-                    b[i + 2] = v.z;
-                    b[i + 3] = v.w;
-                } else {
-                    b[i] = bias[min(e0 + i, E - 1)];
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) b[i] = 0.f;
-        }
-        // (experts past the last: minus infinity, read from the row's end)
-        if constexpr (VEC) {
-#pragma unroll
-            for (int i = 0; i < EPL; i += 4) {
-                const float4 v = *reinterpret_cast<const float4*>(from + min(e0 + i, E - 4));
-                c[i] = v.x;
-                c[i + 1] = v.y;
-                c[i + 2] = v.z;
-                c[i + 3] = v.w;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) c[i] = from[min(e0 + i, E - 1)];
-        }
+        float c[EPL], s[EPL];
         uint32_t gone = ~0u << min(max(E - e0, 0), EPL);  // bit i: expert e0 + i is out
         asm volatile("" : "+v"(gone));       // (keeps masks made of it out of scalar registers)
+        load_experts<EPL, VEC>(from, e0, E, c);
+        // (experts past the last: minus infinity)
         if (e0 + EPL > E) {
 #pragma unroll
             for (int i = 0; i < EPL; ++i) c[i] = gone >> i & 1 ? -INFINITY : c[i];
@@ -431,7 +467,13 @@ __global__ __launch_bounds__(256, EPL == 16 && !VEC ? 3 : 4) void route_scored_k
         }
         if (!by_logit) {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) c[i] = s[i] + b[i];
+            for (int i = 0; i < EPL; ++i) c[i] = s[i];
+            if (bias != nullptr) {
+                float b[EPL];
+                load_experts<EPL, VEC>(bias, e0, E, b);
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) c[i] += b[i];
+            }
         }
         bool sure = true;
         bool dropped = false;                // the lane's experts are out
@@ -492,14 +534,12 @@ __global__ __launch_bounds__(256, EPL == 16 && !VEC ? 3 : 4) void route_scored_k
             wave_lds();
             if (!by_logit) sure = apart(low, high, most);
         }
-        double list[EPL];
+        double list[EPL > KM ? EPL : KM];
 #pragma unroll
         for (int i = 0; i < EPL; ++i) list[i] = key_of(gone >> i & 1 ? kOut : key_high(c[i]), e0 + i);
-        sort8(list);
-        if constexpr (EPL == 16) {
-            sort8(list + 8);
-            merge8(list, list + 8);
-        }
+        sort_lane<KM, EPL>(list);
+#pragma unroll
+        for (int i = EPL; i < KM; ++i) list[i] = key_of(kOut, 255);
         if (whole_lanes) {
             // the group's two largest, from the lists' heads
             const bool live = e0 < E;
@@ -525,18 +565,18 @@ __global__ __launch_bounds__(256, EPL == 16 && !VEC ? 3 : 4) void route_scored_k
                 sure = apart(live && !dropped ? v : INFINITY, live && dropped ? v : -INFINITY,
                              live ? fmaxf(fabsf(a), fabsf(a2)) : 0.f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) list[i] = dropped ? key_of(kOut, e0 + i) : list[i];
+            for (int i = 0; i < KM; ++i) list[i] = dropped ? key_of(kOut, 255) : list[i];
         }
-        merge_partner<0>(list);
-        merge_partner<1>(list);
-        if constexpr (G >= 8) merge_partner<2>(list);
-        if constexpr (G >= 16) merge_partner<3>(list);
-        // list: the token's 8 largest, in every lane
+        merge_partner<0, KM>(list);
+        merge_partner<1, KM>(list);
+        if constexpr (G >= 8) merge_partner<2, KM>(list);
+        if constexpr (G >= 16) merge_partner<3, KM>(list);
+        // list: the token's KM largest, in every lane
         if (!by_logit) {
             float last = 0.f, most = 0.f;
             float gap = INFINITY;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < KM; ++j) {
                 const float v = key_value(list[j]);
                 if (j < k) {
                     if (j > 0) gap = fminf(gap, last - v);
@@ -553,8 +593,8 @@ __global__ __launch_bounds__(256, EPL == 16 && !VEC ? 3 : 4) void route_scored_k
             near = reduce<G>(dropped ? 0 : near, Add());
             sure = sure && gap > tol && near <= k;
         }
-        // gates: lane j has slot j (and j + G)
-        constexpr int SLOTS = G >= 8 ? 1 : 2;
+        // gates: lane j has slots j, j + G, ..
+        constexpr int SLOTS = KM > G ? KM / G : 1;
         float chosen[SLOTS];
         int id[SLOTS];
         float total = 0.f;
@@ -562,7 +602,7 @@ __global__ __launch_bounds__(256, EPL == 16 && !VEC ? 3 : 4) void route_scored_k
         for (int u = 0; u < SLOTS; ++u) {
             double mine = list[0];
 #pragma unroll
-            for (int j = 1; j < 8; ++j) mine = s_lane + u * G == j ? list[j] : mine;
+            for (int j = 1; j < KM; ++j) mine = s_lane + u * G == j ? list[j] : mine;
             id[u] = key_index(mine);
             chosen[u] = 0.f;
             if (s_lane + u * G < k) {
@@ -829,12 +869,16 @@ namespace {
 // hold the experts, 8 each, 16 each beyond 128 (wider lists, fewer steps between lanes).
 int lanes_for(int E) { return E <= 32 ? 4 : (E <= 64 ? 8 : 16); }
 
+// More than fits a list (32768 x 256: k = 16 33 us by lists, k = 24 120 us by waves), or
+// rows shorter than a load.
+bool whole_wave(const moe_gating_t& g) { return g.k > kMaxList || g.E < 4; }
+
 }  // namespace
 
 // Workgroups: one round of tokens each up to 1024 of them, then up to kMaxRounds
 // (each lane adds that many scores in 32 bits).
 int64_t route_scored_blocks(const moe_gating_t& g) {
-    const int64_t per_round = g.k <= 8 ? 4 * (64 / lanes_for(g.E)) : 4;
+    const int64_t per_round = whole_wave(g) ? 4 : 4 * (64 / lanes_for(g.E));
     const int64_t rounds = ceil_div(g.T, per_round);
     return std::max(std::min<int64_t>(rounds, 1024), ceil_div(rounds, kMaxRounds));
 }
@@ -847,17 +891,24 @@ hipError_t launch_route_scored(const moe_gating_t& g, const float* logits, const
     if (blocks > 0) {
         const unsigned grid = static_cast<unsigned>(blocks);
         const bool vec = g.E % 4 == 0;
-#define MOE_ROUTE(G, EPL)                                                                                      \
-    do {                                                                                                       \
-        if (vec) route_scored_kernel<G, EPL, true><<<grid, 256, 0, s>>>(g, logits, bias, ids, gates, sums);      \
-        else route_scored_kernel<G, EPL, false><<<grid, 256, 0, s>>>(g, logits, bias, ids, gates, sums);         \
+#define MOE_ROUTE_K(G, EPL, VEC)                                                                                    \
+    do {                                                                                                            \
+        if (g.k <= 4) route_scored_kernel<G, EPL, VEC, 4><<<grid, 256, 0, s>>>(g, logits, bias, ids, gates, sums);    \
+        else if (g.k <= 8) route_scored_kernel<G, EPL, VEC, 8><<<grid, 256, 0, s>>>(g, logits, bias, ids, gates, sums); \
+        else route_scored_kernel<G, EPL, VEC, kMaxList><<<grid, 256, 0, s>>>(g, logits, bias, ids, gates, sums);      \
     } while (0)
-        if (g.k > 8) route_scored_wave_kernel<<<grid, 256, 0, s>>>(g, logits, bias, ids, gates, sums);
+#define MOE_ROUTE(G, EPL)                        \
+    do {                                         \
+        if (vec) MOE_ROUTE_K(G, EPL, true);      \
+        else MOE_ROUTE_K(G, EPL, false);         \
+    } while (0)
+        if (whole_wave(g)) route_scored_wave_kernel<<<grid, 256, 0, s>>>(g, logits, bias, ids, gates, sums);
         else if (g.E <= 32) MOE_ROUTE(4, 8);
         else if (g.E <= 64) MOE_ROUTE(8, 8);
         else if (g.E <= 128) MOE_ROUTE(16, 8);
         else MOE_ROUTE(16, 16);
 #undef MOE_ROUTE
+#undef MOE_ROUTE_K
     }
     if (score_sums != nullptr)
         score_sums_kernel<<<static_cast<unsigned>(ceil_div(g.E, 8)), 1024, 0, s>>>(partial, blocks, g.E, score_sums);

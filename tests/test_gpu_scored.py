@@ -215,8 +215,7 @@ def test_softmax_without_bias_is_route():
 def test_workspace_is_enough_and_undefined():
     T, E = 700, 48
     l = gpu(logits_of(T, E, 12))
-    g = moe.api._gating(T, E, 4, "softmax", 1, None, 2, True, 1.0)
-    n = moe.route_scored_workspace_size(g)
+    n = moe.route_scored_workspace_size(T, E, 4)
     buf = torch.full((n + 4096,), 0xFF, dtype=torch.uint8, device=DEV)
     a = moe.route_scored(4, logits=l, with_score_sums=True, ws=buf[:n])
     assert (buf[n:] == 0xFF).all()
