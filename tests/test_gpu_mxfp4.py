@@ -15,7 +15,17 @@ WIDTHS = [(8, 32), (64, 256), (72, 96), (136, 288), (256, 1056), (520, 64), (100
 LARGE = {
     "ragged": ([1900, 0, 1, 2500, 300, 3491], 2056, 544),
     "one queue": ([4100], 4104, 224),
+    # more tiles of 256 than twice the CUs, of several slices, the last not whole: over
+    # and under 8 columns of tiles
+    "stream": ([2900, 1, 0, 2555, 3556], 4360, 800),
+    "stream of few columns": ([20001, 300, 19000], 1032, 544),
 }
+# (kernel, rows, E, N, K)
+CHOICES = [("split32", 11, 3, 1440, 480), ("split32", 327, 17, 16, 608), ("split64", 505, 8, 824, 2400),
+           ("split64", 1399, 3, 360, 1952), ("tile64x128", 1209, 17, 32, 32), ("tile64x128", 4487, 3, 304, 1408),
+           ("tile64x128", 33, 17, 1680, 96), ("tile128", 663, 1, 3312, 64), ("tile128", 4079, 17, 440, 800),
+           ("tile128", 2475, 3, 864, 2272), ("tile256", 5437, 8, 2168, 992), ("tile256", 2211, 3, 5512, 1216)]
+DENSE = [(1, 8, 32), (1, 4096, 2048), (16, 1000, 8224), (33, 136, 131104), (300, 520, 4096), (4100, 2056, 544)]
 
 
 def gpu(a):
@@ -160,9 +170,22 @@ def test_product_large(queues, dtype):
     product(quantised(3, R, K), quantised(4, len(counts), N, K), off, N, dtype, what=queues)
 
 
+def ragged(rows, E, seed):
+    w = np.random.default_rng(seed).random(E) ** 2
+    c = np.floor(rows * w / w.sum()).astype(int)
+    c[0] += rows - c.sum()
+    return c.tolist()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("rows,N,K", [(1, 8, 32), (1, 4096, 2048), (16, 1000, 8224), (33, 136, 131104), (300, 520, 4096),
-                                      (4100, 2056, 544)])
+@pytest.mark.parametrize("kernel,rows,E,N,K", CHOICES)
+def test_every_kernel(kernel, rows, E, N, K, dtype):
+    off = offsets_of(ragged(rows - 7, E, seed=rows), start=3)
+    product(quantised(20, rows, K), quantised(21, E, N, K), off, N, dtype, what=kernel)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,N,K", DENSE)
 def test_dense(rows, N, K, dtype):
     product(quantised(5, rows, K), quantised(6, N, K), None, N, dtype, what=f"dense {rows} {N}x{K}")
 
