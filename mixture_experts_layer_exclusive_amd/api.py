@@ -17,12 +17,17 @@ from . import _lib as L
 
 _DTYPES = {torch.float32: L.MOE_DTYPE_F32, torch.bfloat16: L.MOE_DTYPE_BF16}
 
+# (looked up once: a small call spends as long in the binding as on the GPU)
+_Tensor = torch.Tensor
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
 
 def _expect(name: str, t: Optional[torch.Tensor], shape, dtype, device=None, required: bool = True):
     """Checks one tensor argument against the problem before anything reaches
     the C ABI (which sees only pointers: a wrong shape or dtype there would
     make the kernels read or write out of bounds)."""
-    if (type(t) is torch.Tensor and t.shape == shape and t.dtype == dtype and
+    if (type(t) is _Tensor and t.dtype is dtype and t.shape == shape and
             (device is None or t.device == device) and t.is_contiguous()):
         return  # (the usual case, in under a microsecond)
     if t is None:
@@ -72,11 +77,14 @@ def _launch(device: torch.device, where: str, fn, *args):
     """Calls an entry point of the C ABI with the current stream of ``device``
     as its last argument; ``device`` is current meanwhile (a kernel starts on
     the current device)."""
-    if device.index == torch._C._cuda_getDevice():
-        L.check(fn(*args, torch._C._cuda_getCurrentRawStream(device.index)), where)
+    index = device.index
+    if index == _current_device():
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            L.check(fn(*args, torch._C._cuda_getCurrentRawStream(device.index)), where)
+            status = fn(*args, _raw_stream(index))
+    if status:
+        L.check(status, where)
 
 
 def _on_gpu(device: torch.device):
@@ -431,11 +439,11 @@ def combine_backward(dy: torch.Tensor, assign_pos: torch.Tensor, gates: torch.Te
     if not with_dy_perm:
         res["dy_perm"] = None
     elif res.get("dy_perm") is None:
-        res["dy_perm"] = torch.empty((T * k, d), dtype=dt, device=dev)
+        res["dy_perm"] = dy.new_empty((T * k, d))
     if not with_dgates:
         res["dgates"] = None
     elif res.get("dgates") is None:
-        res["dgates"] = torch.empty((T, k), dtype=torch.float32, device=dev)
+        res["dgates"] = gates.new_empty((T, k))
     _on_gpu(dev)
     p = L.MoeProblem(T, d, k, k, 64, _DTYPES[dt])
     _launch(dev, "moe_combine_backward", L.load().moe_combine_backward, ctypes.byref(p), dy.data_ptr(),
@@ -830,11 +838,11 @@ def quantize_rows_mxfp4(src: torch.Tensor, codes: Optional[torch.Tensor] = None,
     dt = _float_dtype("src", src)
     _expect("src", src, (rows, cols), dt)
     if codes is None:
-        codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev)
+        codes = src.new_empty((rows, cols // 2), dtype=torch.uint8)
     else:
         _expect("codes", codes, (rows, cols // 2), torch.uint8, dev)
     if scales is None:
-        scales = torch.empty((_mxfp4_slices(cols), rows, 8), dtype=torch.uint8, device=dev)
+        scales = src.new_empty((_mxfp4_slices(cols), rows, 8), dtype=torch.uint8)
     else:
         _expect("scales", scales, (_mxfp4_slices(cols), rows, 8), torch.uint8, dev)
     _on_gpu(dev)
@@ -856,7 +864,7 @@ def dequantize_rows_mxfp4(codes: torch.Tensor, scales: torch.Tensor, dtype=torch
     _expect("codes", codes, (rows, cols // 2), torch.uint8)
     _expect("scales", scales, (_mxfp4_slices(cols), rows, 8), torch.uint8, dev)
     if out is None:
-        out = torch.empty((rows, cols), dtype=dtype, device=dev)
+        out = codes.new_empty((rows, cols), dtype=dtype)
     else:
         _expect("out", out, (rows, cols), dtype, dev)
     _on_gpu(dev)
@@ -888,7 +896,7 @@ def grouped_matmul_mxfp4(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tenso
     _expect("w_scales", w_scales, (S, *w.shape[:-1], 8), torch.uint8, dev)
     _expect("offsets", offsets, (E + 1,), torch.int32, dev, required=False)
     if c is None:
-        c = torch.empty((R, N), dtype=out_dtype, device=dev)
+        c = a.new_empty((R, N), dtype=out_dtype)
     else:
         _expect("c", c, (R, N), out_dtype, dev)
     _on_gpu(dev)

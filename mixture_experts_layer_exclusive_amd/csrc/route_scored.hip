@@ -261,6 +261,7 @@ __device__ __forceinline__ void choose64(const moe_gating_t& g, const float* __r
         wave_lds();
         for (int q = lane; q < g.groups; q += 64) {
             double a = -DBL_MAX, b = -DBL_MAX;
+#pragma unroll 8
             for (int e = q * size; e < (q + 1) * size; ++e) {
                 const double v = c_of[e];
                 b = fmax(b, fmin(a, v));
@@ -276,6 +277,7 @@ __device__ __forceinline__ void choose64(const moe_gating_t& g, const float* __r
             if (e >= E) continue;
             const int mine = e / size;
             int rank = 0;
+#pragma unroll 8
             for (int q = 0; q < g.groups; ++q) rank += before(v_of[q], q, v_of[mine], mine) ? 1 : 0;
             if (rank >= g.groups_kept) c[j] = -DBL_MAX;
         }
@@ -494,6 +496,7 @@ __global__ __launch_bounds__(256, KM == 16 || (EPL == 16 && !VEC) ? 3 : 4) void 
             float most = 0.f;
             for (int q = s_lane; q < g.groups; q += G) {
                 float a = -INFINITY, a2 = -INFINITY;
+#pragma unroll 8
                 for (int i = 0; i < size; ++i) {
                     const float v = c_of[q * size + i];
                     a2 = fmaxf(a2, fminf(a, v));
@@ -510,6 +513,7 @@ __global__ __launch_bounds__(256, KM == 16 || (EPL == 16 && !VEC) ? 3 : 4) void 
             for (int q = s_lane; q < g.groups; q += G, ++n) {
                 const float v = v_of[q];
                 int rank = 0;
+#pragma unroll 8
                 for (int o = 0; o < g.groups; ++o) rank += v_of[o] > v || (v_of[o] == v && o < q) ? 1 : 0;
                 if (rank < g.groups_kept) {
                     stay[n / 32] |= 1u << (n & 31);
@@ -525,7 +529,10 @@ __global__ __launch_bounds__(256, KM == 16 || (EPL == 16 && !VEC) ? 3 : 4) void 
             int q = e0 / size, r = e0 - q * size;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
-                if (v_of[min(q, g.groups - 1)] == 0.f) gone |= 1u << i;
+                if (v_of[min(q, g.groups - 1)] == 0.f) {
+                    gone |= 1u << i;
+                    c[i] = -INFINITY;
+                }
                 if (++r == size) {
                     r = 0;
                     ++q;
@@ -573,25 +580,24 @@ __global__ __launch_bounds__(256, KM == 16 || (EPL == 16 && !VEC) ? 3 : 4) void 
         if constexpr (G >= 16) merge_partner<3, KM>(list);
         // list: the token's KM largest, in every lane
         if (!by_logit) {
-            float last = 0.f, most = 0.f;
-            float gap = INFINITY;
+            // (the list falls: its ends bound |c|, and if the last is above minus infinity all are)
+            const float first = key_value(list[0]);
+            float last = first, gap = INFINITY;
 #pragma unroll
-            for (int j = 0; j < KM; ++j) {
-                const float v = key_value(list[j]);
+            for (int j = 1; j < KM; ++j) {
                 if (j < k) {
-                    if (j > 0) gap = fminf(gap, last - v);
-                    most = fmaxf(most, fabsf(v));
-                    if (!(v > -INFINITY)) gap = 0.f;  // (differences of infinities are no numbers)
+                    const float v = key_value(list[j]);
+                    gap = fminf(gap, last - v);
                     last = v;
                 }
             }
-            const float tol = s_error + 0x1p-22f * most;
-            // no others within the error of the last
+            const float tol = s_error + 0x1p-22f * fmaxf(fabsf(first), fabsf(last));
+            // no others within the error of the last (of those that are out c is minus infinity)
             int near = 0;
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) near += !(gone >> i & 1) && !(c[i] < last - tol) ? 1 : 0;
+            for (int i = 0; i < EPL; ++i) near += !(c[i] < last - tol) ? 1 : 0;
             near = reduce<G>(dropped ? 0 : near, Add());
-            sure = sure && gap > tol && near <= k;
+            sure = sure && last > -INFINITY && gap > tol && near <= k;
         }
         // gates: lane j has slots j, j + G, ..
         constexpr int SLOTS = KM > G ? KM / G : 1;
