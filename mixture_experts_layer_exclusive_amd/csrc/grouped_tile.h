@@ -303,8 +303,12 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
     // (there and back over X, so that two products in a row share a fragment: 1 %)
     auto mul = [&](int kk, int q) {
         const int mb = q / MB % 2 ? MB - 1 - q % MB : q % MB;
-        if constexpr (MX) multiply_mx4(kk, f[kk][MB + q / MB], f[kk][mb], scale[MB + q / MB], scale[mb], acc[q / MB][mb]);
-        else multiply<TY>(f[kk][MB + q / MB], f[kk][mb], acc[q / MB][mb]);
+        if constexpr (MX) {
+            multiply_mx4(kk, f[kk][MB + q / MB], f[kk][mb], scale[MB + q / MB], scale[mb], acc[q / MB][mb]);
+            // (stays here: the compiler sinks these products below the branches that follow,
+            // away from the loads and reads that they are to hide)
+            asm volatile("" : "+a"(acc[q / MB][mb]));
+        } else multiply<TY>(f[kk][MB + q / MB], f[kk][mb], acc[q / MB][mb]);
     };
 
     // the refilling loads go out over SLOTS MFMAs: those of step 1 after FREE,
