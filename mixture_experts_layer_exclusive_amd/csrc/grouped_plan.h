@@ -145,6 +145,15 @@ Plan plan_for(const moe_grouped_t& g, int mode, bool int8) {
 constexpr Cost kCostMx4[kVariants] = {{4, 161}, {15, 288}, {0, 0}, {37, 123}, {36, 191}, {93, 520}};
 Plan plan_mxfp4(const moe_grouped_t& g) { return plan_of(g, kNT, false, kCostMx4, 256); }
 
+// Whether it goes to the kernel for reductions of one slice: where the queues are short,
+// too, and a tile of 64 rows or more is mostly start and end.  Both sides: 75 queues of 2
+// rows, 10816 x 64, 11 us, the best other kernel 61; 255 of 12 rows, 12000 x 96, 63 and 200;
+// 200 of 60 rows, 12000 x 128, 197 and 213; 16 of 50 rows, 5600 x 256, 12.9 and 12.2; 200 of
+// 100 rows, 1600 x 256, 47 and 40.
+bool short_mxfp4(const moe_grouped_t& g) {
+    return g.K <= 256 && g.rows <= 64 * std::min<int64_t>(g.E, g.rows);
+}
+
 size_t parts_bytes(const moe_grouped_t& g, const Plan& p) {
     return p.parts > 1 ? static_cast<size_t>(p.parts) * g.E * g.N * g.K * 4 : 0;
 }

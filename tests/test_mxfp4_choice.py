@@ -18,11 +18,11 @@ int main() {
     int E, N, K, f32;
     while (scanf("%ld %d %d %d %d", &rows, &E, &N, &K, &f32) == 5) {
         const moe_grouped_t g{rows, E, N, K, f32 ? MOE_DTYPE_F32 : MOE_DTYPE_BF16};
-        printf("%d\n", static_cast<int>(plan_mxfp4(g).v));
+        printf("%d\n", short_mxfp4(g) ? 9 : static_cast<int>(plan_mxfp4(g).v));
     }
 }
 """
-SPLIT32, SPLIT64, TILE64X128, TILE128, TILE256 = 0, 1, 3, 4, 5
+SPLIT32, SPLIT64, TILE64X128, TILE128, TILE256, SHORT = 0, 1, 3, 4, 5, 9
 
 
 def sizes():
@@ -62,11 +62,12 @@ def variants(tmp_path_factory):
 def test_every_kernel_is_compared_with_the_oracle(variants):
     for f32 in (0, 1):
         seen = set(variants([(*s, f32) for s in sizes()]))
-        assert seen == {SPLIT32, SPLIT64, TILE64X128, TILE128, TILE256}
+        assert seen == {SPLIT32, SPLIT64, TILE64X128, TILE128, TILE256, SHORT}
 
 
 def test_sizes_meant_for_a_kernel_take_it(variants):
-    names = dict(split32=SPLIT32, split64=SPLIT64, tile64x128=TILE64X128, tile128=TILE128, tile256=TILE256)
+    names = dict(split32=SPLIT32, split64=SPLIT64, tile64x128=TILE64X128, tile128=TILE128, tile256=TILE256,
+                 short=SHORT)
     for name, rows, E, N, K in CHOICES:
         for f32 in (0, 1):
             assert variants([(rows, E, N, K, f32)]) == [names[name]], (name, rows, E, N, K)
