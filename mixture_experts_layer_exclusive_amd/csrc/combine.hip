@@ -113,20 +113,27 @@ __global__ __launch_bounds__(256) void combine_f32_kernel(const float* __restric
 
 // ---- the gradient --------------------------------------------------------------
 //
-// One workgroup per token: a thread keeps its columns of dy, and of KM slots at a
-// time reads y_perm's rows, adds to the slots' products and writes dy_perm's rows.
-// The products' sums over the workgroup are taken at the end, in a fixed order.
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
+// L lanes per token, 256 / L tokens per workgroup: a thread keeps its columns of dy, and of
+// KM slots at a time reads y_perm's rows, adds to the slots' products and writes dy_perm's
+// rows.  The products' sums over the lanes are taken at the end, in a fixed order.
+// A float32 row starts at any multiple of 4 bytes and is moved 16 bytes at a time all the
+// same; its last chunk starts 4 values before its end and leaves those that the chunk
+// before it has out of the sums (and writes the same values to them again).
+// Rows of more than 64 lanes are read and written past the caches, short ones (whose ends
+// share cache lines) are read through them, those of 16 lanes also written (30000 tokens,
+// 8 slots of 33 floats: 19 us for 27; 512 floats and more gain nothing).
+// Bound by memory: 32768 tokens, 8 slots of 2048 bf16, 2.28 GB in 394 to 426 us (5.4 to 5.8
+// TB/s, a copy 6.0), 449 with 4 slots at a time through the caches; 30000 tokens of 128 bf16
+// 23 us, at a copy's rate 22.6; 1023 floats, whose rows begin inside cache lines, 10000
+// tokens 149, at a copy's rate 118.
+typedef float f32x4_any_t __attribute__((ext_vector_type(4), aligned(4)));  // at any float
 
 // Rows read and written once go past the caches.
 __device__ __forceinline__ void store_nt(uint4* p, const uint4& v) {
     const u32x4_t w = {v.x, v.y, v.z, v.w};
     __builtin_nontemporal_store(w, reinterpret_cast<u32x4_t*>(p));
 }
-__device__ __forceinline__ void store_nt(float4* p, const float4& v) {
-    const f32x4_t w = {v.x, v.y, v.z, v.w};
-    __builtin_nontemporal_store(w, reinterpret_cast<f32x4_t*>(p));
-}
+__device__ __forceinline__ void store_nt(f32x4_any_t* p, const f32x4_any_t& v) { __builtin_nontemporal_store(v, p); }
 __device__ __forceinline__ void store_nt(float* p, float v) { __builtin_nontemporal_store(v, p); }
 
 template <typename T, int V>
@@ -150,19 +157,14 @@ struct Chunk<bf16_t, 8> {
 };
 template <>
 struct Chunk<float, 4> {
-    using Raw = float4;
-    static __device__ __forceinline__ float4 load(const float4* p) {
-        const f32x4_t v = load_nt(reinterpret_cast<const f32x4_t*>(p));
-        return make_float4(v.x, v.y, v.z, v.w);
+    using Raw = f32x4_any_t;
+    static __device__ __forceinline__ f32x4_any_t load(const f32x4_any_t* p) { return __builtin_nontemporal_load(p); }
+    static __device__ __forceinline__ void unpack(const f32x4_any_t& w, float (&v)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = w[i];
     }
-    static __device__ __forceinline__ void unpack(const float4& w, float (&v)[4]) {
-        v[0] = w.x;
-        v[1] = w.y;
-        v[2] = w.z;
-        v[3] = w.w;
-    }
-    static __device__ __forceinline__ float4 scaled(const float (&v)[4], float g) {
-        return make_float4(g * v[0], g * v[1], g * v[2], g * v[3]);
+    static __device__ __forceinline__ f32x4_any_t scaled(const float (&v)[4], float g) {
+        return f32x4_any_t{g * v[0], g * v[1], g * v[2], g * v[3]};
     }
 };
 template <>
@@ -173,15 +175,19 @@ struct Chunk<float, 1> {
     static __device__ __forceinline__ float scaled(const float (&v)[1], float g) { return g * v[0]; }
 };
 
-template <typename T, int V, int KM>
+template <typename T, int V, int KM, int L>
 __global__ __launch_bounds__(256) void combine_backward_kernel(
-    const typename Chunk<T, V>::Raw* __restrict__ dy, const typename Chunk<T, V>::Raw* __restrict__ y_perm,
-    const int32_t* __restrict__ assign_pos, const float* __restrict__ gates, int k, int n, int chunks,
-    typename Chunk<T, V>::Raw* __restrict__ dy_perm, float* __restrict__ dgates) {
+    const T* __restrict__ dy, const T* __restrict__ y_perm, const int32_t* __restrict__ assign_pos,
+    const float* __restrict__ gates, int64_t T_, int k, int n, int d, T* __restrict__ dy_perm,
+    float* __restrict__ dgates) {
     using C = Chunk<T, V>;
-    __shared__ float s_dot[4][KM];
-    const int64_t t = blockIdx.x;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    using Raw = typename C::Raw;
+    const int lane = threadIdx.x & (L - 1), wave = threadIdx.x >> 6;
+    int64_t t = blockIdx.x;
+    if constexpr (L == 64) t = t * 4 + __builtin_amdgcn_readfirstlane(wave);
+    if constexpr (L < 64) t = t * (256 / L) + threadIdx.x / L;
+    if (L < 256 && t >= T_) return;  // (a token's lanes leave together, and meet no barrier)
+    const int chunks = (d + V - 1) / V;
     for (int j0 = 0; j0 < k; j0 += KM) {
         int pos[KM];
         float g[KM], dot[KM];
@@ -192,40 +198,59 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(
             g[j] = j0 + j < k ? gates[t * k + j0 + j] : 0.f;
             dot[j] = 0.f;
         }
-        for (int c = threadIdx.x; c < chunks; c += 256) {
+        for (int c = lane; c < chunks; c += L) {
+            const int at = min(c * V, d - V);
             float a[V];
-            typename C::Raw y[KM];
+            Raw y[KM];
             if (dgates != nullptr) {
 #pragma unroll
                 for (int j = 0; j < KM; ++j)
-                    if (pos[j] >= 0) y[j] = C::load(y_perm + static_cast<int64_t>(pos[j]) * chunks + c);
+                    if (pos[j] >= 0) {
+                        const Raw* const from = reinterpret_cast<const Raw*>(y_perm + static_cast<int64_t>(pos[j]) * d + at);
+                        if constexpr (L == 256) y[j] = C::load(from);
+                        else y[j] = *from;
+                    }
             }
-            C::unpack(dy[t * chunks + c], a);
+            C::unpack(*reinterpret_cast<const Raw*>(dy + t * d + at), a);
 #pragma unroll
             for (int j = 0; j < KM; ++j) {
                 if (pos[j] < 0) continue;
-                const int64_t at = static_cast<int64_t>(pos[j]) * chunks + c;
                 if (dgates != nullptr) {
                     float b[V];
                     C::unpack(y[j], b);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) dot[j] = fmaf(a[i], b[i], dot[j]);
+                    for (int i = 0; i < V; ++i) {
+                        const float sum = fmaf(a[i], b[i], dot[j]);
+                        dot[j] = std::is_same<T, float>::value && i < c * V - at ? dot[j] : sum;
+                    }
                 }
-                if (dy_perm != nullptr) store_nt(dy_perm + at, C::scaled(a, g[j]));
+                if (dy_perm != nullptr) {
+                    Raw* const to = reinterpret_cast<Raw*>(dy_perm + static_cast<int64_t>(pos[j]) * d + at);
+                    if constexpr (L >= 64) store_nt(to, C::scaled(a, g[j]));
+                    else *to = C::scaled(a, g[j]);
+                }
             }
         }
         if (dgates == nullptr) continue;
 #pragma unroll
-        for (int j = 0; j < KM; ++j) {
+        for (int j = 0; j < KM; ++j)
 #pragma unroll
-            for (int off = 32; off > 0; off >>= 1) dot[j] += __shfl_xor(dot[j], off, 64);
-            if (lane == 0) s_dot[wave][j] = dot[j];
+            for (int off = (L < 64 ? L : 64) / 2; off > 0; off >>= 1) dot[j] += __shfl_xor(dot[j], off, 64);
+        if constexpr (L == 256) {
+            __shared__ float s_dot[4][KM];
+#pragma unroll
+            for (int j = 0; j < KM; ++j)
+                if ((threadIdx.x & 63) == 0) s_dot[wave][j] = dot[j];
+            __syncthreads();
+            if (threadIdx.x < KM && j0 + threadIdx.x < k)
+                dgates[t * k + j0 + threadIdx.x] = (s_dot[0][threadIdx.x] + s_dot[1][threadIdx.x]) +
+                                                   (s_dot[2][threadIdx.x] + s_dot[3][threadIdx.x]);
+            __syncthreads();
+        } else {
+#pragma unroll
+            for (int j = 0; j < KM; ++j)
+                if (lane == j && j0 + j < k) dgates[t * k + j0 + j] = dot[j];
         }
-        __syncthreads();
-        if (threadIdx.x < KM && j0 + threadIdx.x < k)
-            dgates[t * k + j0 + threadIdx.x] = (s_dot[0][threadIdx.x] + s_dot[1][threadIdx.x]) +
-                                               (s_dot[2][threadIdx.x] + s_dot[3][threadIdx.x]);
-        __syncthreads();
     }
 }
 
@@ -233,17 +258,31 @@ template <typename T, int V>
 hipError_t start_combine_backward(const moe_problem_t& p, const void* dy, const void* y_perm,
                                   const int32_t* assign_pos, const float* gates, void* dy_perm, float* dgates,
                                   hipStream_t s) {
-    using Raw = typename Chunk<T, V>::Raw;
-    const unsigned grid = static_cast<unsigned>(p.T);
     const int n = static_cast<int>(p.T * p.k);
-    auto start = [&](auto km) {
-        combine_backward_kernel<T, V, decltype(km)::value><<<grid, 256, 0, s>>>(
-            static_cast<const Raw*>(dy), static_cast<const Raw*>(y_perm), assign_pos, gates, p.k, n, p.d / V,
-            static_cast<Raw*>(dy_perm), dgates);
+    auto start = [&](auto km, auto lanes) {
+        constexpr int kLanes = decltype(lanes)::value;
+        const unsigned grid = static_cast<unsigned>((p.T + 256 / kLanes - 1) / (256 / kLanes));
+        combine_backward_kernel<T, V, decltype(km)::value, kLanes><<<grid, 256, 0, s>>>(
+            static_cast<const T*>(dy), static_cast<const T*>(y_perm), assign_pos, gates, p.T, p.k, n, p.d,
+            static_cast<T*>(dy_perm), dgates);
     };
-    if (p.k <= 2) start(std::integral_constant<int, 2>{});
-    else if (p.k <= 4) start(std::integral_constant<int, 4>{});
-    else start(std::integral_constant<int, 8>{});
+    auto with_lanes = [&](auto lanes) {
+        if (p.k <= 2) start(std::integral_constant<int, 2>{}, lanes);
+        else if (p.k <= 4) start(std::integral_constant<int, 4>{}, lanes);
+        else start(std::integral_constant<int, 8>{}, lanes);
+    };
+    // As many lanes as the row can use.  30000 tokens, 8 slots, with 16, 64 and 256 lanes:
+    // 64 bf16 (8 chunks) 16, 27 and 66 us, 128 27, 31 and 66, 192 40, 40 and 66, 256 52, 50
+    // and 68, 512 (64 chunks) 101, 96 and 89; 33 floats 27, 40 and 84, 130 120, 74 and 96;
+    // 100 tokens of 512 bf16 7.7, 4.9 and 4.7 (all past the caches).
+    const int chunks = (p.d + V - 1) / V;
+    if constexpr (V == 1) {  // (fewer than 4 floats)
+        with_lanes(std::integral_constant<int, 16>{});
+    } else {
+        if (chunks <= 16) with_lanes(std::integral_constant<int, 16>{});
+        else if (chunks <= 48) with_lanes(std::integral_constant<int, 64>{});
+        else with_lanes(std::integral_constant<int, 256>{});
+    }
     return hipGetLastError();
 }
 
@@ -254,7 +293,7 @@ hipError_t launch_combine_backward(const moe_problem_t& p, const void* dy, const
                                    hipStream_t s) {
     if (p.dtype == MOE_DTYPE_BF16)
         return start_combine_backward<bf16_t, 8>(p, dy, y_perm, assign_pos, gates, dy_perm, dgates, s);
-    if (p.d % 4 == 0) return start_combine_backward<float, 4>(p, dy, y_perm, assign_pos, gates, dy_perm, dgates, s);
+    if (p.d >= 4) return start_combine_backward<float, 4>(p, dy, y_perm, assign_pos, gates, dy_perm, dgates, s);
     return start_combine_backward<float, 1>(p, dy, y_perm, assign_pos, gates, dy_perm, dgates, s);
 }
 

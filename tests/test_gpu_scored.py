@@ -358,6 +358,36 @@ def test_combine_backward_tokens(T):
     check_combine(T, 2, 36, torch.float32, seed=T)
 
 
+@pytest.mark.parametrize("d", [2, 3, 4, 5, 6, 63, 64, 65, 67, 190, 192, 193, 255, 257])
+def test_combine_backward_short_rows(d):
+    """Rows of any number of floats, each beginning at any float, by 16, 64 and 256 lanes."""
+    for T, k in ((1, 1), (17, 2), (33, 3), (101, 8), (5, 9)):
+        check_combine(T, k, d, torch.float32, seed=d + T, away=0.2)
+
+
+@pytest.mark.parametrize("d", [64, 128, 320, 384, 448])
+def test_combine_backward_short_rows_bf16(d):
+    for T, k in ((1, 1), (17, 2), (33, 3), (101, 8), (5, 9)):
+        check_combine(T, k, d, torch.bfloat16, seed=d + T, away=0.2)
+
+
+@pytest.mark.parametrize("d", [5, 6, 7, 67, 257, 1027])
+def test_combine_backward_counts_every_column_once(d):
+    """Small whole numbers, whose sums are exact, and an infinity in the columns that two
+    loads hold."""
+    rng = np.random.default_rng(d)
+    T, k = 9, 2
+    dy, y = (rng.integers(-4, 5, s).astype(np.float32) for s in ((T, d), (T * k, d)))
+    pos = rng.permutation(T * k).astype(np.int32)
+    y[pos[0], d - 4:] = dy[0, d - 4:] = 1.0
+    y[pos[0], d - 4] = np.inf
+    gates = np.ones((T, k), np.float32)
+    g = moe.combine_backward(gpu(dy), gpu(pos), gpu(gates), y_perm=gpu(y))
+    want = np.einsum("td,tkd->tk", dy, y[pos].reshape(T, k, d))
+    assert np.isinf(want[0, 0]) and np.array_equal(g["dgates"].cpu().numpy(), want)
+    assert np.array_equal(g["dy_perm"].cpu().numpy()[pos], np.repeat(dy, k, 0))
+
+
 def test_combine_backward_with_experts_elsewhere():
     check_combine(50, 4, 128, torch.bfloat16, away=0.4)
     check_combine(50, 4, 10, torch.float32, away=1.0)
