@@ -369,7 +369,11 @@ __global__ __launch_bounds__(256) void route_scored_wave_kernel(moe_gating_t g, 
 // certain if all that it compared differs by more than 2^-20 (softmax: 2^-18 max s) + 2^-22
 // max |c|, twice that for groups (sums of two), else it is made again in 64 bits.
 //
-// 32768 tokens, 256 experts: see the launch below.
+// Bound by instructions (about 1000 for the 4 tokens of a wave, a third of them the lists'),
+// not by the logits' bytes: 32768 tokens, 256 experts, k = 8: 14 us by logits or scores (6 us
+// for the bytes at a copy's rate), 20 with a bias, 24 in 8 groups, of which 4 the certainty's
+// checks and a few tokens' second choice, and 29 with score sums; one token 5.3 us.  A whole
+// wave per token in 64 bits took 161 us.
 constexpr int kMaxList = 16;    // the longest list: larger k go to the whole wave's choice
 constexpr int kMaxRounds = 32;  // of tokens that a workgroup takes one after the other
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -412,6 +416,13 @@ __global__ __launch_bounds__(256, KM == 16 || (EPL == 16 && !VEC) ? 3 : 4) void 
     constexpr int BUF = TPW * EMAX > 2 * MOE_MAX_EXPERTS ? TPW * EMAX : 2 * MOE_MAX_EXPERTS;
     __shared__ double s_buf[4][BUF];
     __shared__ uint64_t s_again[4][kMaxRounds];
+    // the bias, where its loads would have to be moved as the logits' are (39008 tokens, 250
+    // experts: 50 us for 40)
+    __shared__ alignas(16) float s_bias[VEC ? 4 : EMAX];
+    if (!VEC && bias != nullptr) {
+        for (int e = threadIdx.x; e < EMAX; e += 256) s_bias[e] = e < g.E ? bias[e] : 0.f;
+        __syncthreads();
+    }
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int row = lane / G, s_lane = lane % G;
     const int E = g.E, k = g.k;
@@ -472,9 +483,19 @@ __global__ __launch_bounds__(256, KM == 16 || (EPL == 16 && !VEC) ? 3 : 4) void 
             for (int i = 0; i < EPL; ++i) c[i] = s[i];
             if (bias != nullptr) {
                 float b[EPL];
-                load_experts<EPL, VEC>(bias, e0, E, b);
+                if constexpr (VEC) {
+                    load_experts<EPL, VEC>(bias, e0, E, b);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < EPL; ++i) b[i] = s_bias[e0 + i];
+                }
 #pragma unroll
                 for (int i = 0; i < EPL; ++i) c[i] += b[i];
+            }
+            // (again: neither a score of zero nor what was loaded past the bias is near a choice)
+            if (e0 + EPL > E) {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) c[i] = gone >> i & 1 ? -INFINITY : c[i];
             }
         }
         bool sure = true;
@@ -698,7 +719,8 @@ __global__ __launch_bounds__(1024) void score_sums_kernel(const float* __restric
 //
 // G lanes per token, 8 experts each; lane j takes slots j, j + G, .. and leaves u in LDS
 // under its expert.  Bound by the logits read and the gradients written: whole 16-byte
-// words, two tokens of 256 experts in flight per wave.  Without dscore_sums all but the
+// words, two tokens of 256 experts in flight per wave (32768 x 256: 18 us, 3.8 TB/s; one token
+// per wave in 4-byte words 42 us).  Without dscore_sums all but the
 // chosen experts' gradients are zero (softmax: if renormalised), and only their logits
 // are read.
 template <int G, typename T, typename F>
