@@ -12,7 +12,12 @@ for the special cases, closed forms and invariants), and every function in
 differences, an independent automatic differentiation, linearity), and
 every function in ``moe_fp8`` by ``tests/test_oracle_fp8_pins.py`` (torch's
 float8 conversion, exhaustive code round trip, brute-force nearest code,
-exact arithmetic on representable inputs).  No function here is "parity
+exact arithmetic on representable inputs), every function in
+``moe_grouped`` by ``tests/test_oracle_grouped_pins.py``, in ``moe_scored`` by
+``tests/test_oracle_scored_pins.py`` (torch's softmax, sigmoid, top-k and
+automatic differentiation, finite differences), and in ``moe_mxfp4`` by
+``tests/test_oracle_mxfp4_pins.py`` (the format's definition, exhaustive code
+round trip, rounding borders, exact products).  No function here is "parity
 unpinned".
 """
 from .moe_oracle import (  # noqa: F401
