@@ -113,7 +113,7 @@ __global__ __launch_bounds__(256) void combine_f32_kernel(const float* __restric
 
 // ---- the gradient --------------------------------------------------------------
 //
-// L lanes per token, 256 / L tokens per workgroup: a thread keeps its columns of dy, and of
+// L lanes per token, 256 / L tokens per workgroup (1024 lanes: one): a thread keeps its columns of dy, and of
 // KM slots at a time reads y_perm's rows, adds to the slots' products and writes dy_perm's
 // rows.  The products' sums over the lanes are taken at the end, in a fixed order.
 // A float32 row starts at any multiple of 4 bytes and is moved 16 bytes at a time all the
@@ -176,7 +176,7 @@ struct Chunk<float, 1> {
 };
 
 template <typename T, int V, int KM, int L>
-__global__ __launch_bounds__(256) void combine_backward_kernel(
+__global__ __launch_bounds__(L > 256 ? L : 256) void combine_backward_kernel(
     const T* __restrict__ dy, const T* __restrict__ y_perm, const int32_t* __restrict__ assign_pos,
     const float* __restrict__ gates, int64_t T_, int k, int n, int d, T* __restrict__ dy_perm,
     float* __restrict__ dgates) {
@@ -207,7 +207,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(
                 for (int j = 0; j < KM; ++j)
                     if (pos[j] >= 0) {
                         const Raw* const from = reinterpret_cast<const Raw*>(y_perm + static_cast<int64_t>(pos[j]) * d + at);
-                        if constexpr (L == 256) y[j] = C::load(from);
+                        if constexpr (L >= 256) y[j] = C::load(from);
                         else y[j] = *from;
                     }
             }
@@ -236,15 +236,18 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(
         for (int j = 0; j < KM; ++j)
 #pragma unroll
             for (int off = (L < 64 ? L : 64) / 2; off > 0; off >>= 1) dot[j] += __shfl_xor(dot[j], off, 64);
-        if constexpr (L == 256) {
-            __shared__ float s_dot[4][KM];
+        if constexpr (L >= 256) {
+            __shared__ float s_dot[L / 64][KM];
 #pragma unroll
             for (int j = 0; j < KM; ++j)
                 if ((threadIdx.x & 63) == 0) s_dot[wave][j] = dot[j];
             __syncthreads();
-            if (threadIdx.x < KM && j0 + threadIdx.x < k)
-                dgates[t * k + j0 + threadIdx.x] = (s_dot[0][threadIdx.x] + s_dot[1][threadIdx.x]) +
-                                                   (s_dot[2][threadIdx.x] + s_dot[3][threadIdx.x]);
+            if (threadIdx.x < KM && j0 + threadIdx.x < k) {
+                float total = 0.f;
+#pragma unroll
+                for (int w = 0; w < L / 64; ++w) total += s_dot[w][threadIdx.x];
+                dgates[t * k + j0 + threadIdx.x] = total;
+            }
             __syncthreads();
         } else {
 #pragma unroll
@@ -261,8 +264,9 @@ hipError_t start_combine_backward(const moe_problem_t& p, const void* dy, const 
     const int n = static_cast<int>(p.T * p.k);
     auto start = [&](auto km, auto lanes) {
         constexpr int kLanes = decltype(lanes)::value;
-        const unsigned grid = static_cast<unsigned>((p.T + 256 / kLanes - 1) / (256 / kLanes));
-        combine_backward_kernel<T, V, decltype(km)::value, kLanes><<<grid, 256, 0, s>>>(
+        constexpr int kThreads = kLanes > 256 ? kLanes : 256, kTokens = kThreads / kLanes;
+        const unsigned grid = static_cast<unsigned>((p.T + kTokens - 1) / kTokens);
+        combine_backward_kernel<T, V, decltype(km)::value, kLanes><<<grid, kThreads, 0, s>>>(
             static_cast<const T*>(dy), static_cast<const T*>(y_perm), assign_pos, gates, p.T, p.k, n, p.d,
             static_cast<T*>(dy_perm), dgates);
     };
@@ -274,14 +278,17 @@ hipError_t start_combine_backward(const moe_problem_t& p, const void* dy, const 
     // As many lanes as the row can use.  30000 tokens, 8 slots, with 16, 64 and 256 lanes:
     // 64 bf16 (8 chunks) 16, 27 and 66 us, 128 27, 31 and 66, 192 40, 40 and 66, 256 52, 50
     // and 68, 512 (64 chunks) 101, 96 and 89; 33 floats 27, 40 and 84, 130 120, 74 and 96;
-    // 100 tokens of 512 bf16 7.7, 4.9 and 4.7 (all past the caches).
+    // 100 tokens of 512 bf16 7.7, 4.9 and 4.7 (all past the caches).  And a token per
+    // compute unit with 256 and 1024 lanes: 38 tokens, 8 slots of 7168 floats 18 and 10 us,
+    // 200 of 4096 floats 17 and 12, of 2048 9.6 and 7.9; 500 of 2048 14 and 16.
     const int chunks = (p.d + V - 1) / V;
     if constexpr (V == 1) {  // (fewer than 4 floats)
         with_lanes(std::integral_constant<int, 16>{});
     } else {
         if (chunks <= 16) with_lanes(std::integral_constant<int, 16>{});
         else if (chunks <= 48) with_lanes(std::integral_constant<int, 64>{});
-        else with_lanes(std::integral_constant<int, 256>{});
+        else if (chunks <= 256 || p.T > 256) with_lanes(std::integral_constant<int, 256>{});
+        else with_lanes(std::integral_constant<int, 1024>{});
     }
     return hipGetLastError();
 }

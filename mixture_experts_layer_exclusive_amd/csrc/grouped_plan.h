@@ -69,8 +69,9 @@ struct Plan {
 };
 
 // The cheapest variant for mode `mode` of problem g.  The host knows the queues'
-// number and sum only: a queue is taken to end in half a tile.
-Plan plan_of(const moe_grouped_t& g, int mode, bool f32, const Cost* cost, int64_t qs) {
+// number and sum only: a queue is taken to end in half a tile (with `one`, not a
+// single queue, whose rows it knows).
+Plan plan_of(const moe_grouped_t& g, int mode, bool f32, const Cost* cost, int64_t qs, bool one = false) {
     const int64_t M = g.N, P = mode == kNT ? g.N : g.K;
     const int64_t live = std::max<int64_t>(std::min<int64_t>(g.E, g.rows), 1);
     Plan best{kTile128, 1, 0};
@@ -116,8 +117,9 @@ Plan plan_of(const moe_grouped_t& g, int mode, bool f32, const Cost* cost, int64
             const int64_t n = ceil_div(mode == kNT ? g.K : g.N, qs);
             // row tiles: a queue's last one is half full in the mean, and their
             // number varies by sqrt(live / 12); rounds: the mean over that spread
-            const double mt = static_cast<double>(g.rows) / kTileM[v] + 0.5 * live;
-            const double spread = std::sqrt(live / 12.0);
+            const bool known = one && g.E == 1;
+            const double mt = known ? ceil_div(g.rows, kTileM[v]) : static_cast<double>(g.rows) / kTileM[v] + 0.5 * live;
+            const double spread = known ? 0.0 : std::sqrt(live / 12.0);
             const double low = std::max<double>(live, mt - spread), high = std::max<double>(live, mt + spread);
             const double rounds = 0.5 * (std::ceil(low * pt / kCus) + std::ceil(high * pt / kCus));
             const double t = rounds * round_time(v, n, out_bytes);
@@ -141,9 +143,11 @@ Plan plan_for(const moe_grouped_t& g, int mode, bool int8) {
 // the best variant in the mean, 23 % in one of 100 (with bf16's costs 2.7 %).  Both sides:
 // 512 rows, 4096 x 4096, tiles of 64 x 128 12.5 us, of 128 15.2 us; 2048 rows, of 128 22.8,
 // of 256 29.6; 16384 rows, 14336 x 4096, in 8 queues, of 128 622, of 256 506; 128 rows, split
-// tiles of 32 9.1, tiles of 64 x 128 11.7.
+// tiles of 32 9.1, tiles of 64 x 128 11.7.  (A single queue with half a tile more, as many:
+// 2048 rows, 4096 x 2048, in 3 rounds of 128 or one of 256, 20.7 us; known to be 2 rounds,
+// 16.6.)
 constexpr Cost kCostMx4[kVariants] = {{4, 161}, {15, 288}, {0, 0}, {37, 123}, {36, 191}, {93, 520}};
-Plan plan_mxfp4(const moe_grouped_t& g) { return plan_of(g, kNT, false, kCostMx4, 256); }
+Plan plan_mxfp4(const moe_grouped_t& g) { return plan_of(g, kNT, false, kCostMx4, 256, true); }
 
 // Whether it goes to the kernel for reductions of one slice: where the queues are short,
 // too, and a tile of 64 rows or more is mostly start and end.  Both sides: 75 queues of 2
