@@ -129,6 +129,12 @@ hipError_t start(const moe_grouped_t& g, const void* a, const void* sa, const vo
         case kTile64x128:
             grouped_tile_kernel<kMx4, kNT, 1, 2, 2, O><<<grid, 256, 0, s>>>(a, w, offsets, g.E, rows, g.N, K, C, sa, sw, 1);
             break;
+        case kHalves64x128:
+            grouped_tile_kernel<kMx4, kNT, 1, 2, 2, O, 2><<<grid, 512, 0, s>>>(a, w, offsets, g.E, rows, g.N, K, C, sa, sw, 1);
+            break;
+        case kHalves128:
+            grouped_tile_kernel<kMx4, kNT, 2, 2, 2, O, 2><<<grid, 512, 0, s>>>(a, w, offsets, g.E, rows, g.N, K, C, sa, sw, 1);
+            break;
         case kTile256:
             grouped_tile_kernel<kMx4, kNT, 4, 4, 2, O><<<grid, 256, 0, s>>>(a, w, offsets, g.E, rows, g.N, K, C, sa, sw, 1);
             break;

@@ -25,9 +25,10 @@ int64_t row_tiles(const moe_grouped_t& g, int bm) {
 }
 
 // The kernels and their tiles (rows x columns).
-enum Variant { kSplit32, kSplit64, kTile64, kTile64x128, kTile128, kTile256, kVariants };
-constexpr int kTileM[kVariants] = {32, 64, 64, 64, 128, 256};
-constexpr int kTileN[kVariants] = {32, 64, 64, 128, 128, 256};
+// kHalves..: tiles whose slices two halves of the workgroup take in turn.
+enum Variant { kSplit32, kSplit64, kTile64, kTile64x128, kTile128, kTile256, kHalves64x128, kHalves128, kVariants };
+constexpr int kTileM[kVariants] = {32, 64, 64, 64, 128, 256, 64, 128};
+constexpr int kTileN[kVariants] = {32, 64, 64, 128, 128, 256, 128, 128};
 
 // What a round of one tile per CU takes, in 10 ns: for every slice, and once
 // (start, epilogue), and no less than its stores.  Fitted to sweeps of rows,
@@ -43,6 +44,7 @@ constexpr int kTileN[kVariants] = {32, 64, 64, 128, 128, 256};
 // tiles of 32 in 2 rounds 17 us, tiles of 128 in one round 33 us.
 struct Cost {
     int slice, once;
+    int alone;  // for every slice, where a CU has one tile and nothing beside it to do (4-bit values)
 };
 constexpr Cost kCost16[kVariants] = {{9, 100}, {25, 300}, {0, 0}, {30, 200}, {48, 170}, {148, 400}};
 // float32 is bound by its matrix instructions: 64 x 64 tiles are as fast per
@@ -57,7 +59,8 @@ constexpr int kCus = 256;
 constexpr int kMaxParts = 32;
 
 // What each mode and type has.
-bool has(Variant v, int mode, bool f32) {
+bool has(Variant v, int mode, bool f32, bool mx4) {
+    if (v == kHalves64x128 || v == kHalves128) return mx4;
     if (mode == kTN) return v == kTile128 || v == kTile256 || (f32 && v == kTile64);
     return f32 ? v == kSplit32 || v == kTile64 : v != kTile64;
 }
@@ -69,9 +72,9 @@ struct Plan {
 };
 
 // The cheapest variant for mode `mode` of problem g.  The host knows the queues'
-// number and sum only: a queue is taken to end in half a tile (with `one`, not a
-// single queue, whose rows it knows).
-Plan plan_of(const moe_grouped_t& g, int mode, bool f32, const Cost* cost, int64_t qs, bool one = false) {
+// number and sum only: a queue is taken to end in half a tile (with `mx4`, 4-bit
+// values, not a single queue, whose rows it knows).
+Plan plan_of(const moe_grouped_t& g, int mode, bool f32, const Cost* cost, int64_t qs, bool mx4 = false) {
     const int64_t M = g.N, P = mode == kNT ? g.N : g.K;
     const int64_t live = std::max<int64_t>(std::min<int64_t>(g.E, g.rows), 1);
     Plan best{kTile128, 1, 0};
@@ -84,7 +87,7 @@ Plan plan_of(const moe_grouped_t& g, int mode, bool f32, const Cost* cost, int64
     const int out_bytes = g.dtype == MOE_DTYPE_BF16 ? 2 : 4;
     for (int i = 0; i < kVariants; ++i) {
         const Variant v = static_cast<Variant>(i);
-        if (!has(v, mode, f32)) continue;
+        if (!has(v, mode, f32, mx4)) continue;
         const int64_t pt = ceil_div(P, kTileN[v]);
         if (mode == kTN) {
             const int64_t whole = g.E * ceil_div(M, kTileM[v]) * pt;
@@ -117,12 +120,13 @@ Plan plan_of(const moe_grouped_t& g, int mode, bool f32, const Cost* cost, int64
             const int64_t n = ceil_div(mode == kNT ? g.K : g.N, qs);
             // row tiles: a queue's last one is half full in the mean, and their
             // number varies by sqrt(live / 12); rounds: the mean over that spread
-            const bool known = one && g.E == 1;
+            const bool known = mx4 && g.E == 1;
             const double mt = known ? ceil_div(g.rows, kTileM[v]) : static_cast<double>(g.rows) / kTileM[v] + 0.5 * live;
             const double spread = known ? 0.0 : std::sqrt(live / 12.0);
             const double low = std::max<double>(live, mt - spread), high = std::max<double>(live, mt + spread);
             const double rounds = 0.5 * (std::ceil(low * pt / kCus) + std::ceil(high * pt / kCus));
-            const double t = rounds * round_time(v, n, out_bytes);
+            const double alone = rounds < 2 ? (2 - rounds) * cost[v].alone * static_cast<double>(n) : 0.0;
+            const double t = rounds * round_time(v, n, out_bytes) + alone;
             if (least == 0 || t < least) {
                 least = t;
                 best = Plan{v, 1, row_tiles(g, kTileM[v]) * pt};
@@ -138,15 +142,22 @@ Plan plan_for(const moe_grouped_t& g, int mode, bool int8) {
     return plan_of(g, mode, f32, cost, int8 ? 128 : (f32 ? 32 : 64));
 }
 
-// The forward of 4-bit floats.  Fitted to 20000 random products (E 1 to 256, rows per
-// queue 1 to 60000, N 64 to 14400, K 128 to 9600), of which the choice is 0.8 % slower than
-// the best variant in the mean, 23 % in one of 100 (with bf16's costs 2.7 %).  Both sides:
-// 512 rows, 4096 x 4096, tiles of 64 x 128 12.5 us, of 128 15.2 us; 2048 rows, of 128 22.8,
-// of 256 29.6; 16384 rows, 14336 x 4096, in 8 queues, of 128 622, of 256 506; 128 rows, split
-// tiles of 32 9.1, tiles of 64 x 128 11.7.  (A single queue with half a tile more, as many:
-// 2048 rows, 4096 x 2048, in 3 rounds of 128 or one of 256, 20.7 us; known to be 2 rounds,
-// 16.6.)
-constexpr Cost kCostMx4[kVariants] = {{4, 161}, {15, 288}, {0, 0}, {37, 123}, {36, 191}, {93, 520}};
+// The forward of 4-bit floats.  Fitted to 47000 random products (E 1 to 256, rows per
+// queue 1 to 60000, N 64 to 14400, K 128 to 9600), of which the choice is 0.5 % slower than
+// the best variant in the mean, 15 to 18 % in one of 100 (with bf16's costs 2.7 %).  Both
+// sides: 512 rows, 4096 x 4096, tiles of 64 x 128 12.5 us, of 128 15.2 us; 2048 rows, of 128
+// 22.8, of 256 29.6; 16384 rows, 14336 x 4096, in 8 queues, of 128 622, of 256 506; 128 rows,
+// split tiles of 32 9.1, tiles of 64 x 128 11.7.  (A single queue with half a tile more, as
+// many: 2048 rows, 4096 x 2048, in 3 rounds of 128 or one of 256, 20.7 us; known to be 2
+// rounds, 16.6.)
+// A tile alone on its CU takes longer than its loads or its products: the 4 waves wait for
+// each other at every step (a ring of 3, 4 or 5 stages changes nothing).  Two halves, each
+// with its own slices and stages, fill the waits: 599 rows, 4456 x 8512, tiles of 128 25 us
+// for 31; 375, 7744 x 4096, 14.4 and 17.5; 113, 8656 x 2496, tiles of 64 x 128 9.9 and 11.1.
+// Short reductions keep the whole tiles, two of which share a CU: 113 rows, 11312 x 1472, 9.2
+// us either way.
+constexpr Cost kCostMx4[kVariants] = {{4, 163, 0},  {12, 401, 0}, {0, 0, 0},    {28, 123, 11},
+                                      {28, 178, 14}, {60, 490, 0}, {27, 164, 4}, {27, 270, 3}};
 Plan plan_mxfp4(const moe_grouped_t& g) { return plan_of(g, kNT, false, kCostMx4, 256, true); }
 
 // Whether it goes to the kernel for reductions of one slice: where the queues are short,

@@ -38,12 +38,17 @@ namespace {
 // 28 1541, 36 1498, 52 1463).  Before step 3 the next slice has landed, and
 // step 3 reads its first fragments.
 //
+// HALVES = 2 (512 threads): the slices of one tile dealt in turn to two halves of the
+// workgroup, each a workgroup as above with its own stages; the second's sums are added
+// to the first's at the end.  Both pass every barrier together; of an odd number of slices
+// the second half's last is out of range.
+//
 // The largest tiles at a long reduction are bound by power first: products of
 // normal values from registers alone hold 1.8 GHz (16384 rows, 14336 x 4096:
 // 1045 us), of zeros 2.4 GHz (786 us), and this kernel 1.5 GHz.  One queue of
 // those rows takes 1358 us; 1334 over operands from the caches only, 1332
 // without half of the fragment reads.  8 queues of 2048: 1428, 1328, 1406.
-template <int MB, int NB, int NS, typename O, bool MX = false>
+template <int MB, int NB, int NS, typename O, bool MX = false, int HALVES = 1>
 struct TileLds {
     static constexpr int OPERANDS = 64 * (MB + NB) * 128;
     // (4-bit values) loads of scales per wave and slice, 16 bytes per lane where they
@@ -58,22 +63,22 @@ struct TileLds {
     // outputs beside the stages; the others take one tile and stage over them
     static constexpr bool STREAM = MB * NB > 4;
     static constexpr int EPI_AT = STREAM ? NS * STAGE : 0;
-    static constexpr int Q_AT = NS * STAGE + (STREAM ? 4 * EPI : 0);
+    static constexpr int Q_AT = HALVES * NS * STAGE + (STREAM ? 4 * EPI : 0);
     static_assert(4 * EPI <= NS * STAGE, "the staged outputs must fit the stages");
     static constexpr int RING_AT = Q_AT + sizeof(Queues);
-    static constexpr int DEAL_AT = RING_AT + 512;
+    static constexpr int DEAL_AT = RING_AT + HALVES * 512;
     static constexpr int BYTES = DEAL_AT + (STREAM ? sizeof(Deal) : 0);
     static_assert(BYTES <= 160 * 1024, "LDS");
 };
 
 // smem: TileLds::BYTES, 1024-byte aligned; workgroup `block` of `blocks`
-template <int TY, int MODE, int MB, int NB, int NS, typename O>
+template <int TY, int MODE, int MB, int NB, int NS, typename O, int HALVES = 1>
 __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block, int blocks, const void* __restrict__ Xp,
                                              const void* __restrict__ Yp, const int32_t* __restrict__ offsets, int E,
                                              int rows, int N, int K, O* __restrict__ C, const void* __restrict__ sx,
                                              const void* __restrict__ sy, int parts) {
     constexpr bool MX = TY == kMx4;
-    using Lds = TileLds<MB, NB, NS, O, MX>;
+    using Lds = TileLds<MB, NB, NS, O, MX, HALVES>;
     constexpr bool XC = MODE == kTN;             // X column-major
     constexpr bool YC = MODE != kNT;             // Y column-major
     static_assert((TY != kI8 && TY != kMx4) || MODE == kNT, "codes: forward only");
@@ -97,10 +102,12 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
     constexpr bool STREAM = Lds::STREAM;
     constexpr int EPI_AT = Lds::EPI_AT, Q_AT = Lds::Q_AT;
     Queues& queues = *reinterpret_cast<Queues*>(smem + Q_AT);
+    static_assert(HALVES == 1 || (HALVES == 2 && MX && !STREAM), "two halves: 4-bit values, one tile");
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int half_wg = HALVES == 2 ? __builtin_amdgcn_readfirstlane(tid >> 8) : 0;
+    const int wave = __builtin_amdgcn_readfirstlane(HALVES == 2 ? tid >> 6 & 3 : tid >> 6);  // of the half
     const int wm = wave >> 1, wn = wave & 1;
     const int P = MODE == kNT ? N : K;           // output columns
     const int64_t xrow = static_cast<int64_t>(MODE == kNT ? K : N) * EB;  // bytes of an operand's memory row
@@ -160,6 +167,11 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
     // ---- the load side: the tile being loaded, and how much of it is left
     constexpr int64_t kLineStep = 128;
     const int64_t xstep = XC ? QS * xrow : kLineStep, ystep = YC ? QS * yrow : kLineStep;
+    // the tiles between the load side and the multiplying side (at most two, of
+    // one slice each, and the one being multiplied), kept by each wave for itself
+    int* const ring = reinterpret_cast<int*>(smem + Lds::RING_AT) + (half_wg * 4 + wave) * 32;
+    // (two halves: each its own stages, and slices half_wg, half_wg + 2, ..)
+    smem += half_wg * NS * STAGE;
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
     const uint32_t lds_x = lds0 + wave * (XL * 1024);
     const uint32_t lds_y = lds0 + X_BYTES + wave * (YL * 1024);
@@ -174,14 +186,17 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
     constexpr int SC_LOAD = 64 * Lds::SW, SC_X = 512 * MB;
     const bool sc_y = wave * SL * SC_LOAD >= SC_X;
     const uint32_t sc_off = wave * SL * SC_LOAD - (sc_y ? SC_X : 0) + lane * Lds::SW;
+    const int64_t sc_step = sc_y ? static_cast<int64_t>(E) * N : static_cast<int64_t>(rows);  // rows, a slice on
     uint64_t sc_base = 0;
     uint32_t sc_bytes = 0;                       // of the tile's rows
     static_assert(!MX || SC_X % (SL * SC_LOAD) == 0, "a wave's scales are of one operand");
     uint32_t xoff[XL], yoff[YL], xtail = 0, ytail = 0;
     bool tailed = false;                         // the last slice is not a whole one
+    bool none = false;                           // (two halves) it is past the reduction's end
     auto aim = [&](const Tile& t) {
-        left = slices_of(t);
-        const int qtail = t.q1 - t.q0 - (left - 1) * QS;  // q in the last slice
+        left = (slices_of(t) + HALVES - 1) / HALVES;
+        const int qtail = t.q1 - t.q0 - (HALVES * (left - 1) + half_wg) * QS;  // q in the last slice
+        none = HALVES == 2 && qtail <= 0;
         int ln = lane;
         asm volatile("" : "+v"(ln));  // (keeps the lane's part from being computed ahead and held in registers)
         xtail = ytail = 0;
@@ -202,11 +217,11 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
             yoff[j] = YS::offset(wave * YL + j, ln, static_cast<uint32_t>(yrow), P - t.p0);
             ytail |= (YS::beyond(wave * YL + j, ln, qtail) ? 1u : 0u) << j;
         }
-        xbase = uniform64(xbase);
-        ybase = uniform64(ybase);
+        xbase = uniform64(xbase + half_wg * xstep);
+        ybase = uniform64(ybase + half_wg * ystep);
         if constexpr (MX) {
             const char* const from = static_cast<const char*>(sc_y ? sy : sx);
-            const int64_t row = sc_y ? static_cast<int64_t>(t.e) * N + t.p0 : t.m0;
+            const int64_t row = (sc_y ? static_cast<int64_t>(t.e) * N + t.p0 : t.m0) + half_wg * sc_step;
             sc_base = uniform64(reinterpret_cast<uint64_t>(from + row * 8));
             sc_bytes = __builtin_amdgcn_readfirstlane(8 * (sc_y ? min(TN, P - t.p0) : t.m1 - t.m0));
         }
@@ -220,9 +235,6 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
         for (int j = 0; j < YL; ++j) yoff[j] = kOutOfRange;
         sc_bytes = 0;
     };
-    // the tiles between the load side and the multiplying side (at most two, of
-    // one slice each, and the one being multiplied), kept by each wave for itself
-    int* const ring = reinterpret_cast<int*>(smem + Lds::RING_AT) + wave * 32;
     int loading = 0;                             // tiles the load side has begun
     // the next tile; after the last, every load is out of range
     auto next_load = [&]() {
@@ -264,12 +276,13 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
             for (int j = 0; j < XL; ++j) xoff[j] |= (xtail << (31 - j)) & kOutOfRange;
 #pragma unroll
             for (int j = 0; j < YL; ++j) yoff[j] |= (ytail << (31 - j)) & kOutOfRange;
+            if (none) sc_bytes = 0;
         }
     };
     auto loaded = [&]() {
-        xbase += xstep;
-        ybase += ystep;
-        if constexpr (MX) sc_base += 8 * (sc_y ? static_cast<int64_t>(E) * N : static_cast<int64_t>(rows));
+        xbase += HALVES * xstep;
+        ybase += HALVES * ystep;
+        if constexpr (MX) sc_base += HALVES * 8 * sc_step;
         if (--left == 0) {
             if (STREAM) next_load();
             else nothing();
@@ -288,7 +301,9 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
     int scale[MX ? NR : 1];
     uint2 next_scale[MX ? NR : 1];
     const uint32_t sc_whole = MX ? scale_select(lane >> 5, 8) : 0;
-    const uint32_t sc_last = MX ? scale_select(lane >> 5, (K / 16 - 1) % 8 + 1) : 0;
+    // (two halves: the last slice belongs to the second if their number is even)
+    const bool has_last = HALVES == 1 || ((K + QS - 1) / QS & 1) == 1 - half_wg;
+    const uint32_t sc_last = MX ? scale_select(lane >> 5, has_last ? (K / 16 - 1) % 8 + 1 : 8) : 0;
     const uint32_t sc_at = SC_AT + wm * MB * 256 + (lane & 31) * 8;
     const uint32_t sc_at_y = SC_AT + TM * 8 + wn * NB * 256 + (lane & 31) * 8;
     auto read_scale = [&](int i, uint32_t so) {
@@ -394,6 +409,31 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
         if (!STREAM) {
             wait_vmcnt_lgkm0<0>();
             barrier_lds();
+        }
+        if constexpr (HALVES == 2) {
+            // the second half's sums over its stages, for the first half to add
+            static_assert(4 * NM * 4096 <= NS * STAGE, "the second half's sums must fit its stages");
+            f32x4_t* const part = reinterpret_cast<f32x4_t*>(smem + (1 - half_wg) * NS * STAGE) + wave * (NM * 256) + lane;
+            if (half_wg == 1) {
+#pragma unroll
+                for (int b = 0; b < NM; ++b)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const Acc<TY>& v = acc[b / MB][b % MB];
+                        part[(b * 4 + g) * 64] = f32x4_t{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
+                    }
+            }
+            wait_vmcnt_lgkm0<63>();
+            barrier_lds();
+            if (half_wg == 1) return;
+#pragma unroll
+            for (int b = 0; b < NM; ++b)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const f32x4_t v = part[(b * 4 + g) * 64];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[b / MB][b % MB][4 * g + i] += v[i];
+                }
         }
         const int mrow = t.m0 + wm * MB * 32, pcol = t.p0 + wn * NB * 32;
         float rs[MB];
@@ -533,12 +573,12 @@ __device__ __forceinline__ void grouped_tile(char* __restrict__ smem, int block,
     wait_vmcnt<0>();  // (the last loads still write LDS)
 }
 
-template <int TY, int MODE, int MB, int NB, int NS, typename O>
-__global__ __launch_bounds__(256, (MB * NB > 4 ? 1 : 2)) void grouped_tile_kernel(
+template <int TY, int MODE, int MB, int NB, int NS, typename O, int HALVES = 1>
+__global__ __launch_bounds__(256 * HALVES, (MB * NB > 4 ? 1 : 2)) void grouped_tile_kernel(
     const void* __restrict__ Xp, const void* __restrict__ Yp, const int32_t* __restrict__ offsets, int E, int rows,
     int N, int K, O* __restrict__ C, const void* __restrict__ sx, const void* __restrict__ sy, int parts) {
-    __shared__ __attribute__((aligned(1024))) char smem[TileLds<MB, NB, NS, O, TY == kMx4>::BYTES];
-    grouped_tile<TY, MODE, MB, NB, NS, O>(smem, blockIdx.x, gridDim.x, Xp, Yp, offsets, E, rows, N, K, C, sx, sy, parts);
+    __shared__ __attribute__((aligned(1024))) char smem[TileLds<MB, NB, NS, O, TY == kMx4, HALVES>::BYTES];
+    grouped_tile<TY, MODE, MB, NB, NS, O, HALVES>(smem, blockIdx.x, gridDim.x, Xp, Yp, offsets, E, rows, N, K, C, sx, sy, parts);
 }
 
 // ---- the split kernel ---------------------------------------------------------------
