@@ -116,7 +116,7 @@ hipError_t start(const moe_grouped_t& g, const void* a, const void* sa, const vo
     if (short_mxfp4(g)) return start_short(g, a, sa, w, sw, offsets, C, s);
     const Plan p = plan_mxfp4(g);
     int64_t n = workgroups(g, kNT, p);
-    if (p.v == kTile256) n = std::min<int64_t>(n, align_up(compute_units(s), kXcds));
+    if (p.v == kTile256 || p.v == kTile128x256) n = std::min<int64_t>(n, align_up(compute_units(s), kXcds));
     const unsigned grid = static_cast<unsigned>(n);
     const int rows = static_cast<int>(g.rows), K = g.K / 2;
     switch (p.v) {
@@ -134,6 +134,9 @@ hipError_t start(const moe_grouped_t& g, const void* a, const void* sa, const vo
             break;
         case kHalves128:
             grouped_tile_kernel<kMx4, kNT, 2, 2, 2, O, 2><<<grid, 512, 0, s>>>(a, w, offsets, g.E, rows, g.N, K, C, sa, sw, 1);
+            break;
+        case kTile128x256:
+            grouped_tile_kernel<kMx4, kNT, 2, 4, 2, O><<<grid, 256, 0, s>>>(a, w, offsets, g.E, rows, g.N, K, C, sa, sw, 1);
             break;
         case kTile256:
             grouped_tile_kernel<kMx4, kNT, 4, 4, 2, O><<<grid, 256, 0, s>>>(a, w, offsets, g.E, rows, g.N, K, C, sa, sw, 1);

@@ -26,9 +26,9 @@ int64_t row_tiles(const moe_grouped_t& g, int bm) {
 
 // The kernels and their tiles (rows x columns).
 // kHalves..: tiles whose slices two halves of the workgroup take in turn.
-enum Variant { kSplit32, kSplit64, kTile64, kTile64x128, kTile128, kTile256, kHalves64x128, kHalves128, kVariants };
-constexpr int kTileM[kVariants] = {32, 64, 64, 64, 128, 256, 64, 128};
-constexpr int kTileN[kVariants] = {32, 64, 64, 128, 128, 256, 128, 128};
+enum Variant { kSplit32, kSplit64, kTile64, kTile64x128, kTile128, kTile256, kHalves64x128, kHalves128, kTile128x256, kVariants };
+constexpr int kTileM[kVariants] = {32, 64, 64, 64, 128, 256, 64, 128, 128};
+constexpr int kTileN[kVariants] = {32, 64, 64, 128, 128, 256, 128, 128, 256};
 
 // What a round of one tile per CU takes, in 10 ns: for every slice, and once
 // (start, epilogue), and no less than its stores.  Fitted to sweeps of rows,
@@ -60,7 +60,7 @@ constexpr int kMaxParts = 32;
 
 // What each mode and type has.
 bool has(Variant v, int mode, bool f32, bool mx4) {
-    if (v == kHalves64x128 || v == kHalves128) return mx4;
+    if (v >= kHalves64x128) return mx4;
     if (mode == kTN) return v == kTile128 || v == kTile256 || (f32 && v == kTile64);
     return f32 ? v == kSplit32 || v == kTile64 : v != kTile64;
 }
@@ -142,9 +142,9 @@ Plan plan_for(const moe_grouped_t& g, int mode, bool int8) {
     return plan_of(g, mode, f32, cost, int8 ? 128 : (f32 ? 32 : 64));
 }
 
-// The forward of 4-bit floats.  Fitted to 47000 random products (E 1 to 256, rows per
+// The forward of 4-bit floats.  Fitted to 61000 random products (E 1 to 256, rows per
 // queue 1 to 60000, N 64 to 14400, K 128 to 9600), of which the choice is 0.5 % slower than
-// the best variant in the mean, 15 to 18 % in one of 100 (with bf16's costs 2.7 %).  Both
+// the best variant in the mean, 11 to 17 % in one of 100 (with bf16's costs 2.7 %).  Both
 // sides: 512 rows, 4096 x 4096, tiles of 64 x 128 12.5 us, of 128 15.2 us; 2048 rows, of 128
 // 22.8, of 256 29.6; 16384 rows, 14336 x 4096, in 8 queues, of 128 622, of 256 506; 128 rows,
 // split tiles of 32 9.1, tiles of 64 x 128 11.7.  (A single queue with half a tile more, as
@@ -156,8 +156,12 @@ Plan plan_for(const moe_grouped_t& g, int mode, bool int8) {
 // for 31; 375, 7744 x 4096, 14.4 and 17.5; 113, 8656 x 2496, tiles of 64 x 128 9.9 and 11.1.
 // Short reductions keep the whole tiles, two of which share a CU: 113 rows, 11312 x 1472, 9.2
 // us either way.
-constexpr Cost kCostMx4[kVariants] = {{4, 163, 0},  {12, 401, 0}, {0, 0, 0},    {28, 123, 11},
-                                      {28, 178, 14}, {60, 490, 0}, {27, 164, 4}, {27, 270, 3}};
+// Tiles of 128 x 256, walked as a stream like the largest: between these and those of 128
+// (LDS reads 0.55 of the products' time, those of 128 1.0), and where short reductions of many
+// queues end: 498 rows in 92 queues, 3896 x 352, 14.3 us, the best other 19.3; 3756 in 95,
+// 6632 x 288, 41 and 55; over products whose floor is 5 to 50 us 3 % in the mean.
+constexpr Cost kCostMx4[kVariants] = {{4, 163, 0},  {13, 401, 0}, {0, 0, 0},    {28, 126, 11}, {28, 190, 13},
+                                      {58, 538, 4}, {27, 170, 4}, {26, 275, 4}, {39, 257, 19}};
 Plan plan_mxfp4(const moe_grouped_t& g) { return plan_of(g, kNT, false, kCostMx4, 256, true); }
 
 // Whether it goes to the kernel for reductions of one slice: where the queues are short,

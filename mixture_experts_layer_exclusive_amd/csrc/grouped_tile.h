@@ -53,7 +53,7 @@ struct TileLds {
     static constexpr int OPERANDS = 64 * (MB + NB) * 128;
     // (4-bit values) loads of scales per wave and slice, 16 bytes per lane where they
     // fill one load of each wave, else 4, and the bytes of one
-    static constexpr int SW = MB + NB >= 8 ? 16 : 4;
+    static constexpr int SW = MB + NB >= 6 ? 16 : 4;
     static constexpr int SL = MX ? (512 * (MB + NB) + 4 * 64 * SW - 1) / (4 * 64 * SW) : 0;
     static constexpr int STAGE = OPERANDS + SL * 4 * 64 * SW;
     static constexpr int NP = sizeof(O) == 2 && NB >= 2 ? 2 : 1;  // column blocks the epilogue stages at a time

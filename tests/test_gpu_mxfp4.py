@@ -26,7 +26,9 @@ CHOICES = [("split32", 11, 3, 1440, 480), ("split32", 327, 17, 16, 608), ("split
            ("tile64x128", 1500, 17, 1680, 96), ("short", 33, 17, 1680, 96), ("short", 300, 5, 520, 160),
            ("short", 900, 17, 1160, 256), ("short", 130, 200, 1000, 224), ("short", 64, 1, 2056, 64),
            ("tile128", 620, 1, 4600, 1056), ("tile128", 4079, 17, 440, 800), ("tile128", 375, 1, 7744, 1120),
-           ("tile256", 5437, 8, 2168, 1248), ("tile256", 2211, 3, 5512, 1216), ("halves64x128", 505, 8, 824, 2400),
+           ("tile256", 5180, 5, 1560, 2560), ("tile256", 2131, 1, 4024, 2496),
+           ("tile128x256", 999, 8, 3400, 1600), ("tile128x256", 1875, 3, 2168, 1568),
+           ("tile128x256", 3662, 1, 1064, 2656), ("halves64x128", 505, 8, 824, 2400),
            ("halves64x128", 1399, 3, 360, 1952), ("halves64x128", 70, 1, 7168, 2368),
            ("halves64x128", 1449, 4, 360, 2816), ("halves128", 2475, 3, 864, 2272),
            ("halves128", 1382, 1, 2168, 2304), ("halves128", 449, 4, 3600, 2816)]

@@ -22,7 +22,7 @@ int main() {
     }
 }
 """
-SPLIT32, SPLIT64, TILE64X128, TILE128, TILE256, HALVES64X128, HALVES128, SHORT = 0, 1, 3, 4, 5, 6, 7, 9
+SPLIT32, SPLIT64, TILE64X128, TILE128, TILE256, HALVES64X128, HALVES128, TILE128X256, SHORT = 0, 1, 3, 4, 5, 6, 7, 8, 9
 
 
 def sizes():
@@ -62,12 +62,13 @@ def variants(tmp_path_factory):
 def test_every_kernel_is_compared_with_the_oracle(variants):
     for f32 in (0, 1):
         seen = set(variants([(*s, f32) for s in sizes()]))
-        assert seen == {SPLIT32, SPLIT64, TILE64X128, TILE128, TILE256, HALVES64X128, HALVES128, SHORT}
+        assert seen == {SPLIT32, SPLIT64, TILE64X128, TILE128, TILE256, HALVES64X128, HALVES128, TILE128X256,
+                        SHORT}
 
 
 def test_sizes_meant_for_a_kernel_take_it(variants):
     names = dict(split32=SPLIT32, split64=SPLIT64, tile64x128=TILE64X128, tile128=TILE128, tile256=TILE256,
-                 short=SHORT, halves64x128=HALVES64X128, halves128=HALVES128)
+                 short=SHORT, halves64x128=HALVES64X128, halves128=HALVES128, tile128x256=TILE128X256)
     for name, rows, E, N, K in CHOICES:
         for f32 in (0, 1):
             assert variants([(rows, E, N, K, f32)]) == [names[name]], (name, rows, E, N, K)
