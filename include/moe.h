@@ -356,8 +356,8 @@ moe_status_t moe_route_scored(const moe_gating_t* g, const void* x, const void* 
  *   sigmoid: dlogits = ds s (1 - s);  softmax: dlogits = s (ds - sum_i s_i ds_i)
  * dlogits [T, E] of dlogits_dtype (a moe_dtype_t value), arithmetic in fp32.
  * The bias has no gradient, and groups do not matter here.  The router's
- * gradients are those of moe_grouped_matmul with one queue of all tokens.  T = 0
- * is a no-op.
+ * gradients are those of moe_grouped_matmul with one queue of all tokens.
+ * dlogits must not overlap the inputs.  T = 0 is a no-op.
  */
 moe_status_t moe_route_scored_backward(const moe_gating_t* g, const float* logits, const int32_t* topk_ids,
                                        const float* dgates, const float* dscore_sums, int32_t dlogits_dtype,
@@ -559,7 +559,8 @@ moe_status_t moe_grouped_matmul_int8(const moe_grouped_t* g, const void* a, cons
  * 255, which stands for NaN, and codes 0: products with it are NaN.  cols
  * must be a positive multiple of 32, at most MOE_GROUPED_MAX_DIM, rows at most
  * 2^24 - 1 and rows * cols at most 2^35 - 2^11 (MOE_ERR_UNSUPPORTED
- * otherwise).  rows = 0 is a no-op.
+ * otherwise).  Outputs must not overlap the input (nor in the two calls
+ * below).  rows = 0 is a no-op.
  */
 moe_status_t moe_quantize_rows_mxfp4(const void* src, int64_t rows, int32_t cols, int32_t dtype, void* codes,
                                      void* scales, void* stream);

@@ -19,8 +19,8 @@ _DTYPES = {torch.float32: L.MOE_DTYPE_F32, torch.bfloat16: L.MOE_DTYPE_BF16}
 
 # (looked up once: a small call spends as long in the binding as on the GPU)
 _Tensor = torch.Tensor
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _expect(name: str, t: Optional[torch.Tensor], shape, dtype, device=None, required: bool = True):
