@@ -264,6 +264,29 @@ def test_broken_offsets_stay_inside():
         assert (guard[0] == 3.0e4).all() and (guard[2] == 3.0e4).all()
 
 
+@pytest.mark.parametrize("kernel,rows,E,N,K", [c for c in CHOICES if c[2] >= 3])
+def test_nan_and_broken_offsets_at_every_kernel(kernel, rows, E, N, K):
+    """As above, at the sizes of every kernel with queues: expert 1's rows and weights are
+    NaN; then offsets that are no offsets, with guards on both sides."""
+    counts = ragged(rows, E, seed=1)
+    off = offsets_of(counts)
+    a, w = quantised(21, rows, K), quantised(22, E, N, K)
+    ac, wc, dense = gpu(a[0]), gpu(w[0].reshape(E, N, -1)), gpu(w[1].reshape(-1, E, N, 8))
+    nan_a, nan_w = gpu(a[1]), dense.clone()
+    nan_a[:, off[1]:off[2]] = 255
+    nan_w[:, 1] = 255
+    c = moe.grouped_matmul_mxfp4(ac, nan_a, wc, nan_w, gpu(off))
+    clean = moe.grouped_matmul_mxfp4(ac, gpu(a[1]), wc, dense, gpu(off))
+    assert torch.isnan(c[off[1]:off[2]]).all()
+    for lo, hi in ((off[0], off[1]), (off[2], off[E])):
+        assert torch.equal(c[lo:hi], clean[lo:hi]) and not torch.isnan(c[lo:hi]).any()
+    guard = torch.full((3, rows, N), 3.0e4, dtype=torch.bfloat16, device=DEV)
+    for bad in ([-5] + [rows // 2, 20] * E, [2 ** 31 - 1] * (E + 1), [0] * E + [2 ** 30]):
+        moe.grouped_matmul_mxfp4(ac, gpu(a[1]), wc, dense, gpu(np.array(bad[:E + 1], np.int32)), c=guard[1])
+        torch.cuda.synchronize()
+        assert (guard[0] == 3.0e4).all() and (guard[2] == 3.0e4).all()
+
+
 def test_same_bits_again_and_captured():
     counts, N, K = [700, 1, 0, 2, 320], 520, 1056
     off, R = gpu(offsets_of(counts)), sum(counts)
