@@ -22,16 +22,16 @@ LARGE = {
 }
 # (kernel, rows, E, N, K)
 CHOICES = [("split32", 11, 3, 1440, 480), ("split32", 327, 17, 16, 608), ("split64", 231, 1, 2744, 3296),
-           ("split64", 225, 1, 2680, 3488), ("tile64x128", 1209, 17, 32, 32), ("tile64x128", 1263, 2, 552, 1248),
+           ("split64", 225, 1, 2680, 3488), ("tile64x128", 1801, 2, 640, 992), ("tile64x128", 1263, 2, 552, 1248),
            ("tile64x128", 1500, 17, 1680, 96), ("short", 33, 17, 1680, 96), ("short", 300, 5, 520, 160),
            ("short", 900, 17, 1160, 256), ("short", 130, 200, 1000, 224), ("short", 64, 1, 2056, 64),
            ("tile128", 620, 1, 4600, 1056), ("tile128", 4079, 17, 440, 800), ("tile128", 375, 1, 7744, 1120),
            ("tile256", 5180, 5, 1560, 2560), ("tile256", 2131, 1, 4024, 2496),
            ("tile128x256", 999, 8, 3400, 1600), ("tile128x256", 1875, 3, 2168, 1568),
-           ("tile128x256", 3662, 1, 1064, 2656), ("halves64x128", 505, 8, 824, 2400),
-           ("halves64x128", 1399, 3, 360, 1952), ("halves64x128", 70, 1, 7168, 2368),
-           ("halves64x128", 1449, 4, 360, 2816), ("halves128", 2475, 3, 864, 2272),
-           ("halves128", 1382, 1, 2168, 2304), ("halves128", 449, 4, 3600, 2816)]
+           ("tile128x256", 3662, 1, 1064, 2656), ("halves64x128", 756, 3, 1184, 3936),
+           ("halves64x128", 264, 5, 2256, 3392), ("halves64x128", 480, 1, 2320, 8704),
+           ("halves64x128", 818, 3, 1552, 4608), ("halves128", 1175, 3, 1832, 4704),
+           ("halves128", 820, 1, 2584, 5120), ("halves128", 642, 1, 3096, 5728)]
 DENSE = [(1, 8, 32), (1, 4096, 2048), (16, 1000, 8224), (33, 136, 131104), (300, 520, 4096), (4100, 2056, 544)]
 
 
