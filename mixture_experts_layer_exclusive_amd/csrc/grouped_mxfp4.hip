@@ -6,7 +6,7 @@
 //
 // To the pipeline a slice is 128 bytes of codes per row, as any type's (256 values here),
 // with 8 scale bytes per row beside it.  Small products are bound by the weights' bytes
-// (64 queues of 6 rows, 2048 x 1408: 98 MB, 21 us) or by a launch's start and end, large ones
+// (64 queues of 6 rows, 2048 x 1408: 98 MB, 23 us) or by a launch's start and end, large ones
 // by matrix products and the card's power: 16384 rows, 14336 x 4096, one queue, 460 us (4180
 // TFLOP/s), K = 14336 1424 us (4730); products alone, from registers, reach 5800 on random
 // codes, 8960 on zeros (unscaled 6470, 9600: a scale costs the instruction 2 cycles in 32).
