@@ -330,10 +330,13 @@ moe_status_t moe_route_scored_workspace_size(const moe_gating_t* g, size_t* byte
  * Equal c, and equal values of groups, go to the lower index.  c is taken
  * in 64 bits (experts whose c differ by less than that resolves may come in
  * either order); without a bias, and without sums over a group, the order is
- * that of the logits.  Scores below 2^-126 may count as 0; chosen scores
- * that are all 0 give gates of 0.  A logit of minus infinity has the score
- * 0, also where all of a token's are (then all scores are 0).  A NaN, in a
- * logit or the bias, is chosen last, and the gates it enters are NaN.
+ * that of the logits.  Scores below 2^-126 may count as 0, but renormalised
+ * gates are the chosen scores' shares however small all of them are, and 0
+ * where all of them are 0: chosen logits of minus infinity, or, of sigmoid
+ * scores, below -709.8 (where exp(-l) overflows 64 bits).  A logit of minus
+ * infinity has the score 0, also where all of a token's are (then all scores
+ * are 0).  A NaN, in a logit or the bias, is chosen last, and the gates it
+ * enters are NaN.
  * Whatever the inputs, a token's ids are k different experts.
  * logits_in, x, w_router and logits_out as in moe_route (bf16 needs d to be
  * a multiple of 64 there).  Limits: E and k as everywhere, T <= 2^24 - 1 and

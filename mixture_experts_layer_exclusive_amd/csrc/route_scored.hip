@@ -320,7 +320,17 @@ __device__ __forceinline__ void choose64(const moe_gating_t& g, const float* __r
             my_e = e;
         }
     }
-    const double total = wave_sum(my_s);
+    double total = wave_sum(my_s);
+    // Scores that vanish even here have the shares of exp(l - most), as 1 - s is 1; but
+    // sigmoid scores that are 0 in 64 bits (logits masked by the type's lowest value) stay 0.
+    if (g.renormalise && total < 0x1p-800 && (total > 0 || g.score == MOE_SCORE_SOFTMAX)) {
+        const double mine = lane < k ? logits[t * E + my_e] : -INFINITY;
+        double most = mine;
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) most = fmax(most, __shfl_xor(most, off, 64));
+        my_s = most == -INFINITY ? 0 : exp(mine - most);
+        total = wave_sum(my_s);
+    }
     if (lane < k) {
         ids[t * k + lane] = my_e;
         const double v = g.renormalise ? (total == 0 ? 0 : my_s / total) : my_s;
@@ -640,6 +650,10 @@ __global__ __launch_bounds__(256, KM == 16 || (EPL == 16 && !VEC) ? 3 : 4) void 
             total += chosen[u];
         }
         total = reduce<G>(total, Add());
+        // Scores chosen by a bias may be denormals or zeros in 32 bits, their shares are not:
+        // such a token's gates are made in 64 bits, with its choice.  (Not a row of minus
+        // infinities, whose softmax scores are zeros in any number of bits.)
+        sure = sure && !(g.renormalise && total < 0x1p-26f && inv != 0.f);
         if (has && sure) {
 #pragma unroll
             for (int u = 0; u < SLOTS; ++u) {
