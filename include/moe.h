@@ -355,7 +355,8 @@ moe_status_t moe_route_scored(const moe_gating_t* g, const void* x, const void* 
  * gates and dscore_sums [E] of the score sums (NULL: zeros):
  *   ds[t, e] = dscore_sums[e] + (e chosen in slot j) scale *
  *     (renormalise ? (dgates[t, j] - sum_i r_i dgates[t, i]) / S : dgates[t, j])
- *     with S = sum of the chosen s and r_i = s_i / S (all 0 if S is 0)
+ *     with S = sum of the chosen s and r_i = s_i / S, the gates' shares (all 0
+ *     where those are)
  *   sigmoid: dlogits = ds s (1 - s);  softmax: dlogits = s (ds - sum_i s_i ds_i)
  * dlogits [T, E] of dlogits_dtype (a moe_dtype_t value), arithmetic in fp32.
  * The bias has no gradient, and groups do not matter here.  The router's

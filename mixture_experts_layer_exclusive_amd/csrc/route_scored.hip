@@ -730,6 +730,10 @@ __global__ __launch_bounds__(1024) void score_sums_kernel(const float* __restric
 //   sigmoid  dl_e = (u_e + s_e ds_e) (1 - s_e)
 //   softmax  dl_e = u_e + s_e (ds_e - sum_i s_i ds_i - sum_j u_j)
 // (s_j / S is one quotient: 1 / S may overflow; renormalised, the u_j add up to zero).
+// A bias may choose experts of scores that are denormals or zeros in 32 bits.  Their r_j are
+// taken of exp(l_j - m), m the largest chosen logit rounded up to a whole number (l_j - m is
+// exact for l_j <= m <= 0; a sigmoid's 1 - s rounds to 1 here), and are 0 where the gates
+// are: sigmoid scores of logits below kLeastLogit.
 //
 // G lanes per token, 8 experts each; lane j takes slots j, j + G, .. and leaves u in LDS
 // under its expert.  Bound by the logits read and the gradients written: whole 16-byte
@@ -751,6 +755,9 @@ __device__ __forceinline__ void sigmoid_parts(float l, float& s, float& rest) {
     rest = l >= 0.f ? x * p : p;
     if (!(l == l)) s = rest = l;
 }
+
+// Sigmoid scores of logits below it are 0 in 64 bits: exp(-l) overflows.
+constexpr float kLeastLogit = -709.78f;
 
 template <int G, bool VEC, typename O>
 __global__ __launch_bounds__(256) void route_scored_backward_kernel(moe_gating_t g, const float* __restrict__ logits,
@@ -857,6 +864,24 @@ __global__ __launch_bounds__(256) void route_scored_backward_kernel(moe_gating_t
     }
     if (g.renormalise) {
         total = reduce_wide<G>(total, Add());
+        const bool small = total < 0x1p-26f;
+        if (__ballot(small) != 0) {
+            float most = -INFINITY, w[SLOTS], sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < SLOTS; ++j) most = fmaxf(most, lc[j]);
+            most = reduce_wide<G>(most, Max());
+            const bool none = softmax ? most == -INFINITY : most < kLeastLogit;
+            most = ceilf(most);
+#pragma unroll
+            for (int j = 0; j < SLOTS; ++j) {
+                w[j] = id[j] < 0 || none ? 0.f : expf(lc[j] - most);
+                sum += w[j];
+            }
+            sum = reduce_wide<G>(sum, Add());
+#pragma unroll
+            for (int j = 0; j < SLOTS; ++j) sc[j] = small ? w[j] : sc[j];
+            total = small ? sum : total;
+        }
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j) {
             sc[j] = total == 0.f ? 0.f : sc[j] / total;

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import mixture_experts_layer_exclusive_amd as moe
-from test_gpu_scored import U, check_route, f64, gpu, logits_of, near
+from test_gpu_scored import U, check_backward, check_route, f64, gpu, logits_of, near
 
 pytestmark = pytest.mark.gpu
 
@@ -95,3 +95,28 @@ def test_sigmoid_gates_that_are_zero_in_64_bits(E, k):
         l = far_logits(E, k, by, E + k)
         ids, gates, _ = moe.route_scored(k, logits=gpu(l), bias=gpu(choosing(E, k)), score="sigmoid")
         assert (torch.sort(ids, 1).values.cpu() == torch.arange(k)).all() and (gates == 0).all()
+
+
+# ---- the gradient ------------------------------------------------------------------
+
+@pytest.mark.parametrize("renormalise", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k", [(3, 2), (24, 4), (62, 7), (128, 12), (256, 8)])
+def test_gradient(E, k, score, renormalise):
+    for by in FAR:
+        l = far_logits(E, k, by, E + k)
+        ids = np.tile(np.random.default_rng(k).permutation(k).astype(np.int32), (len(l), 1))
+        for sums in (True, False):
+            check_backward(l, k, sums=sums, score=score, renormalise=renormalise, ids=ids, scale=2.5)
+
+
+@pytest.mark.parametrize("sums", [True, False])
+def test_gradient_of_gates_that_are_zero(sums):
+    """No gradient through the gates of chosen experts whose scores are all zero: the
+    others' and the sums' only."""
+    for score, value in (("sigmoid", -5000.0), ("sigmoid", np.finfo(np.float32).min), ("sigmoid", -np.inf), ("softmax", -np.inf)):
+        l = logits_of(20, 64, 5)
+        l[:, :6] = value
+        ids = np.tile(np.arange(6, dtype=np.int32), (20, 1))
+        got = check_backward(l, 6, sums=sums, score=score, ids=ids)
+        assert (got[:, :6] == 0).all() and (sums or (got == 0).all())
