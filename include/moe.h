@@ -335,8 +335,8 @@ moe_status_t moe_route_scored_workspace_size(const moe_gating_t* g, size_t* byte
  * where all of them are 0: chosen logits of minus infinity, or, of sigmoid
  * scores, below -709.8 (where exp(-l) overflows 64 bits).  A logit of minus
  * infinity has the score 0, also where all of a token's are (then all scores
- * are 0).  A NaN, in a logit or the bias, is chosen last, and the gates it
- * enters are NaN.
+ * are 0).  A NaN, in a logit or the bias or as a group's sum of infinities of
+ * both signs, is chosen last, and the gates it enters are NaN.
  * Whatever the inputs, a token's ids are k different experts.
  * logits_in, x, w_router and logits_out as in moe_route (bf16 needs d to be
  * a multiple of 64 there).  Limits: E and k as everywhere, T <= 2^24 - 1 and

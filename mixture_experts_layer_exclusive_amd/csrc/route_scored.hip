@@ -267,8 +267,9 @@ __device__ __forceinline__ void choose64(const moe_gating_t& g, const float* __r
                 b = fmax(b, fmin(a, v));
                 a = fmax(a, v);
             }
-            // (a sum with minus infinity is that)
-            v_of[q] = g.group_top == 2 && size > 1 ? fmax(a + b, -1e308) : a;
+            // (a sum with an infinity is that, a sum of both is a NaN and comes last)
+            const double sum = a >= 1e308 && b <= -1e308 ? -1e308 : fmin(fmax(a + b, -1e308), 1e308);
+            v_of[q] = g.group_top == 2 && size > 1 ? sum : a;
         }
         wave_lds();
 #pragma unroll
