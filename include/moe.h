@@ -361,7 +361,9 @@ moe_status_t moe_route_scored(const moe_gating_t* g, const void* x, const void* 
  * dlogits [T, E] of dlogits_dtype (a moe_dtype_t value), arithmetic in fp32.
  * The bias has no gradient, and groups do not matter here.  The router's
  * gradients are those of moe_grouped_matmul with one queue of all tokens.
- * dlogits must not overlap the inputs.  T = 0 is a no-op.
+ * The slots of an expert that a token names more than once (moe_route_scored's
+ * ids do not) add up in their order.  dlogits must not overlap the inputs.  T =
+ * 0 is a no-op.  No atomics: the same inputs give the same bits.
  */
 moe_status_t moe_route_scored_backward(const moe_gating_t* g, const float* logits, const int32_t* topk_ids,
                                        const float* dgates, const float* dscore_sums, int32_t dlogits_dtype,

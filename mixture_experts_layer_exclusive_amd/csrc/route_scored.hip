@@ -809,8 +809,6 @@ __global__ __launch_bounds__(256) void route_scored_backward_kernel(moe_gating_t
                 if (expert(i) < E) ds[i] = dsums[expert(i)];
         }
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i) u_of[s_lane + G * i] = 0.f;
     // the slots: up to MOE_MAX_TOPK / G of them per lane
     constexpr int SLOTS = (MOE_MAX_TOPK + G - 1) / G;
     int id[SLOTS];
@@ -823,6 +821,17 @@ __global__ __launch_bounds__(256) void route_scored_backward_kernel(moe_gating_t
         dg[j] = at < k ? g.scale * dgates[t * k + at] : 0.f;
         lc[j] = id[j] >= 0 ? from[id[j]] : -INFINITY;
     }
+    // whether an expert is in two slots of a token: it keeps one slot's number
+    bool twice = false;
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j)
+        if (id[j] >= 0) u_of[id[j]] = static_cast<float>(s_lane + G * j);
+    wave_lds();
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j) twice |= id[j] >= 0 && u_of[id[j]] != static_cast<float>(s_lane + G * j);
+    wave_lds();
+#pragma unroll
+    for (int i = 0; i < N; ++i) u_of[s_lane + G * i] = 0.f;
     // scores
     float top = -INFINITY, inv = 0.f;
     float s[N], rest[N];
@@ -896,9 +905,19 @@ __global__ __launch_bounds__(256) void route_scored_backward_kernel(moe_gating_t
         if (!g.renormalise) all += u[j];
     }
     wave_lds();
+    if (__ballot(twice) == 0) {
 #pragma unroll
-    for (int j = 0; j < SLOTS; ++j)
-        if (id[j] >= 0) atomicAdd(u_of + id[j], sparse ? u[j] * restc[j] : u[j]);  // (a slot each, but for repeated experts)
+        for (int j = 0; j < SLOTS; ++j)
+            if (id[j] >= 0) u_of[id[j]] = sparse ? u[j] * restc[j] : u[j];
+    } else {
+        // (not what a routing gives: one slot after the other, for sums in their order)
+        for (int q = 0; q < k; ++q) {
+#pragma unroll
+            for (int j = 0; j < SLOTS; ++j)
+                if (s_lane + G * j == q && id[j] >= 0) u_of[id[j]] += sparse ? u[j] * restc[j] : u[j];
+            wave_lds();
+        }
+    }
     if (softmax) {
 #pragma unroll
         for (int i = 0; i < N; ++i) all += s[i] * ds[i];
