@@ -20,6 +20,7 @@
 
 #include "device_util.h"
 #include "moe_internal.h"
+#include "scored_plan.h"
 
 namespace moe {
 
@@ -385,7 +386,6 @@ __global__ __launch_bounds__(256) void route_scored_wave_kernel(moe_gating_t g, 
 // for the bytes at a copy's rate), 20 with a bias, 24 in 8 groups, of which 4 the certainty's
 // checks and a few tokens' second choice, and 29 with score sums; one token 5.3 us.  A whole
 // wave per token in 64 bits took 161 us.
-constexpr int kMaxList = 16;    // the longest list: larger k go to the whole wave's choice
 constexpr int kMaxRounds = 32;  // of tokens that a workgroup takes one after the other
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -950,52 +950,41 @@ __global__ __launch_bounds__(256) void route_scored_backward_kernel(moe_gating_t
 
 }  // namespace
 
-namespace {
-
-// Lanes per token and experts per lane of the 32-bit choice: the fewest lanes that
-// hold the experts, 8 each, 16 each beyond 128 (wider lists, fewer steps between lanes).
-int lanes_for(int E) { return E <= 32 ? 4 : (E <= 64 ? 8 : 16); }
-
-// More than fits a list (32768 x 256: k = 16 33 us by lists, k = 24 120 us by waves), or
-// rows shorter than a load.
-bool whole_wave(const moe_gating_t& g) { return g.k > kMaxList || g.E < 4; }
-
-}  // namespace
-
 // Workgroups: one round of tokens each up to 1024 of them, then up to kMaxRounds
 // (each lane adds that many scores in 32 bits).
 int64_t route_scored_blocks(const moe_gating_t& g) {
-    const int64_t per_round = whole_wave(g) ? 4 : 4 * (64 / lanes_for(g.E));
+    const int64_t per_round = 4 * (64 / route_kernel(g).lanes);
     const int64_t rounds = ceil_div(g.T, per_round);
     return std::max(std::min<int64_t>(rounds, 1024), ceil_div(rounds, kMaxRounds));
 }
 
 hipError_t launch_route_scored(const moe_gating_t& g, const float* logits, const float* bias, int32_t* ids,
                                float* gates, float* score_sums, float* partial, hipStream_t s) {
-    // (without sums nothing is gained by more than one round per workgroup)
     const int64_t blocks = route_scored_blocks(g);
     float* const sums = score_sums != nullptr ? partial : nullptr;
     if (blocks > 0) {
         const unsigned grid = static_cast<unsigned>(blocks);
-        const bool vec = g.E % 4 == 0;
-#define MOE_ROUTE_K(G, EPL, VEC)                                                                                    \
-    do {                                                                                                            \
-        if (g.k <= 4) route_scored_kernel<G, EPL, VEC, 4><<<grid, 256, 0, s>>>(g, logits, bias, ids, gates, sums);    \
-        else if (g.k <= 8) route_scored_kernel<G, EPL, VEC, 8><<<grid, 256, 0, s>>>(g, logits, bias, ids, gates, sums); \
-        else route_scored_kernel<G, EPL, VEC, kMaxList><<<grid, 256, 0, s>>>(g, logits, bias, ids, gates, sums);      \
+        const RouteKernel kernel = route_kernel(g);
+#define MOE_ROUTE_LIST(G, EPL, VEC, KM) route_scored_kernel<G, EPL, VEC, KM><<<grid, 256, 0, s>>>(g, logits, bias, ids, gates, sums)
+#define MOE_ROUTE_K(G, EPL, VEC)                                        \
+    do {                                                                \
+        if (kernel.list == 4) MOE_ROUTE_LIST(G, EPL, VEC, 4);           \
+        else if (kernel.list == 8) MOE_ROUTE_LIST(G, EPL, VEC, 8);      \
+        else MOE_ROUTE_LIST(G, EPL, VEC, kMaxList);                     \
     } while (0)
-#define MOE_ROUTE(G, EPL)                        \
-    do {                                         \
-        if (vec) MOE_ROUTE_K(G, EPL, true);      \
-        else MOE_ROUTE_K(G, EPL, false);         \
+#define MOE_ROUTE(G, EPL)                            \
+    do {                                             \
+        if (kernel.words) MOE_ROUTE_K(G, EPL, true); \
+        else MOE_ROUTE_K(G, EPL, false);             \
     } while (0)
-        if (whole_wave(g)) route_scored_wave_kernel<<<grid, 256, 0, s>>>(g, logits, bias, ids, gates, sums);
-        else if (g.E <= 32) MOE_ROUTE(4, 8);
-        else if (g.E <= 64) MOE_ROUTE(8, 8);
-        else if (g.E <= 128) MOE_ROUTE(16, 8);
+        if (kernel.list == 0) route_scored_wave_kernel<<<grid, 256, 0, s>>>(g, logits, bias, ids, gates, sums);
+        else if (kernel.lanes == 4) MOE_ROUTE(4, 8);
+        else if (kernel.lanes == 8) MOE_ROUTE(8, 8);
+        else if (kernel.per_lane == 8) MOE_ROUTE(16, 8);
         else MOE_ROUTE(16, 16);
 #undef MOE_ROUTE
 #undef MOE_ROUTE_K
+#undef MOE_ROUTE_LIST
     }
     if (score_sums != nullptr)
         score_sums_kernel<<<static_cast<unsigned>(ceil_div(g.E, 8)), 1024, 0, s>>>(partial, blocks, g.E, score_sums);
@@ -1007,15 +996,14 @@ namespace {
 template <typename O>
 void start_backward(const moe_gating_t& g, const float* logits, const int32_t* ids, const float* dgates,
                     const float* dsums, O* dlogits, hipStream_t s) {
-    const int lanes = g.E <= 32 ? 4 : (g.E <= 64 ? 8 : (g.E <= 128 ? 16 : 32));
-    const unsigned grid = static_cast<unsigned>(ceil_div(g.T, 4 * (64 / lanes)));
-    const bool vec = g.E % 4 == 0;
+    const RouteBackKernel kernel = route_back_kernel(g);
+    const unsigned grid = static_cast<unsigned>(ceil_div(g.T, 4 * (64 / kernel.lanes)));
 #define MOE_BACK(G)                                                                                              \
     do {                                                                                                         \
-        if (vec) route_scored_backward_kernel<G, true><<<grid, 256, 0, s>>>(g, logits, ids, dgates, dsums, dlogits); \
+        if (kernel.words) route_scored_backward_kernel<G, true><<<grid, 256, 0, s>>>(g, logits, ids, dgates, dsums, dlogits); \
         else route_scored_backward_kernel<G, false><<<grid, 256, 0, s>>>(g, logits, ids, dgates, dsums, dlogits);    \
     } while (0)
-    switch (lanes) {
+    switch (kernel.lanes) {
         case 4: MOE_BACK(4); break;
         case 8: MOE_BACK(8); break;
         case 16: MOE_BACK(16); break;
