@@ -825,10 +825,11 @@ __global__ __launch_bounds__(256) void route_scored_backward_kernel(moe_gating_t
     bool twice = false;
 #pragma unroll
     for (int j = 0; j < SLOTS; ++j)
-        if (id[j] >= 0) u_of[id[j]] = static_cast<float>(s_lane + G * j);
+        if (G * j < k && id[j] >= 0) u_of[id[j]] = static_cast<float>(s_lane + G * j);
     wave_lds();
 #pragma unroll
-    for (int j = 0; j < SLOTS; ++j) twice |= id[j] >= 0 && u_of[id[j]] != static_cast<float>(s_lane + G * j);
+    for (int j = 0; j < SLOTS; ++j)
+        if (G * j < k && id[j] >= 0) twice |= u_of[id[j]] != static_cast<float>(s_lane + G * j);
     wave_lds();
 #pragma unroll
     for (int i = 0; i < N; ++i) u_of[s_lane + G * i] = 0.f;
@@ -875,7 +876,7 @@ __global__ __launch_bounds__(256) void route_scored_backward_kernel(moe_gating_t
     if (g.renormalise) {
         total = reduce_wide<G>(total, Add());
         const bool small = total < 0x1p-26f;
-        if (__ballot(small) != 0) {
+        if (__builtin_expect(__ballot(small) != 0, 0)) {
             float most = -INFINITY, w[SLOTS], sum = 0.f;
 #pragma unroll
             for (int j = 0; j < SLOTS; ++j) most = fmaxf(most, lc[j]);
@@ -905,7 +906,7 @@ __global__ __launch_bounds__(256) void route_scored_backward_kernel(moe_gating_t
         if (!g.renormalise) all += u[j];
     }
     wave_lds();
-    if (__ballot(twice) == 0) {
+    if (__builtin_expect(__ballot(twice) == 0, 1)) {
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j)
             if (id[j] >= 0) u_of[id[j]] = sparse ? u[j] * restc[j] : u[j];
