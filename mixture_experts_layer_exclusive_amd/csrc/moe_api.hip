@@ -205,7 +205,10 @@ moe_status_t check_gating(const moe_gating_t* g, bool router) {
     if (g->T > INT32_MAX / g->k || g->T > kMaxLaunchItems / 256) return MOE_ERR_UNSUPPORTED;
     if (router) {
         if (g->d < 1 || (g->dtype != MOE_DTYPE_F32 && g->dtype != MOE_DTYPE_BF16)) return MOE_ERR_INVALID_ARGUMENT;
-        if (g->dtype == MOE_DTYPE_BF16 && g->d % 64 != 0) return MOE_ERR_UNSUPPORTED;
+        // The router's kernels count a row's columns (bf16: bytes) in 32 bits.  As wide as
+        // check_problem lets moe_route's be at the smallest f, 64, or one tile of rows.
+        if (g->dtype == MOE_DTYPE_BF16 && (g->d % 64 != 0 || g->d > INT32_MAX / 64)) return MOE_ERR_UNSUPPORTED;
+        if (g->d > 1 << 30) return MOE_ERR_UNSUPPORTED;
     }
     return MOE_OK;
 }
