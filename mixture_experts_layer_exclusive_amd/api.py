@@ -104,7 +104,8 @@ def _addr(t: Optional[torch.Tensor]):
 
 def _int32(where: str, *sizes: int):
     """Refuses sizes past the 32 bits that the ABI takes them in (ctypes would
-    keep their low bits: a row of 2^32 + 64 values would be one of 64)."""
+    keep their low bits: a row of 2^32 + 64 values would be one of 64).  Calls
+    that are not cached compare the sizes of their tensors themselves first."""
     if max(sizes) >= 1 << 31 or min(sizes) < -1 << 31:
         raise L.MoeError(L.MOE_ERR_UNSUPPORTED, where)
 
@@ -113,7 +114,8 @@ def problem(T: int, d: int, E: int, k: int, f: int, dtype) -> L.MoeProblem:
     """The problem statement as the ABI struct; dtype is a torch dtype."""
     if dtype not in _DTYPES:
         raise ValueError(f"unsupported dtype {dtype}")
-    _int32("problem", d, E, k, f)
+    if d >= 1 << 31 or E >= 1 << 31 or k >= 1 << 31 or f >= 1 << 31 or E < 0 or k < 0:
+        _int32("problem", d, E, k, f)
     return L.MoeProblem(T=int(T), d=int(d), E=int(E), k=int(k), f=int(f), dtype=_DTYPES[dtype])
 
 
@@ -445,7 +447,8 @@ def combine_backward(dy: torch.Tensor, assign_pos: torch.Tensor, gates: torch.Te
     res = dict(out or {})
     _expect("dy_perm", res.get("dy_perm"), (T * k, d), dt, dev, required=False)
     _expect("dgates", res.get("dgates"), (T, k), torch.float32, dev, required=False)
-    _int32("moe_combine_backward", d, k)
+    if d >= 1 << 31 or k >= 1 << 31:
+        _int32("moe_combine_backward", d, k)
     if not with_dy_perm:
         res["dy_perm"] = None
     elif res.get("dy_perm") is None:
@@ -608,7 +611,8 @@ def quantize_rows_fp8(src: torch.Tensor, codes: Optional[torch.Tensor] = None,
     rows, cols = src.shape
     dev = src.device
     _expect("src", src, (rows, cols), torch.bfloat16)
-    _int32("moe_quantize_rows_fp8", cols)
+    if cols >= 1 << 31:
+        _int32("moe_quantize_rows_fp8", cols)
     _expect("codes", codes, (rows, cols), torch.uint8, dev, required=False)
     _expect("exps", exps, (rows,), torch.int32, dev, required=False)
     if codes is None:
@@ -786,7 +790,8 @@ def quantize_rows_int8(src: torch.Tensor, codes: Optional[torch.Tensor] = None,
     dev = src.device
     dt = _float_dtype("src", src)
     _expect("src", src, (rows, cols), dt)
-    _int32("moe_quantize_rows_int8", cols)
+    if cols >= 1 << 31:
+        _int32("moe_quantize_rows_int8", cols)
     if codes is None:
         codes = torch.empty((rows, cols), dtype=torch.int8, device=dev)
     else:
@@ -850,7 +855,8 @@ def quantize_rows_mxfp4(src: torch.Tensor, codes: Optional[torch.Tensor] = None,
     dev = src.device
     dt = _float_dtype("src", src)
     _expect("src", src, (rows, cols), dt)
-    _int32("moe_quantize_rows_mxfp4", cols)
+    if cols >= 1 << 31:
+        _int32("moe_quantize_rows_mxfp4", cols)
     if codes is None:
         codes = src.new_empty((rows, cols // 2), dtype=torch.uint8)
     else:
@@ -877,7 +883,8 @@ def dequantize_rows_mxfp4(codes: torch.Tensor, scales: torch.Tensor, dtype=torch
     dev = codes.device
     _expect("codes", codes, (rows, cols // 2), torch.uint8)
     _expect("scales", scales, (_mxfp4_slices(cols), rows, 8), torch.uint8, dev)
-    _int32("moe_dequantize_rows_mxfp4", cols)
+    if cols >= 1 << 31:
+        _int32("moe_dequantize_rows_mxfp4", cols)
     if out is None:
         out = codes.new_empty((rows, cols), dtype=dtype)
     else:
@@ -910,7 +917,8 @@ def grouped_matmul_mxfp4(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tenso
     _expect("w", w, w.shape[:-1] + (half,), torch.uint8, dev)
     _expect("w_scales", w_scales, (S, *w.shape[:-1], 8), torch.uint8, dev)
     _expect("offsets", offsets, (E + 1,), torch.int32, dev, required=False)
-    _int32("moe_grouped_matmul_mxfp4", E, N, 2 * half)
+    if E >= 1 << 31 or N >= 1 << 31 or half >= 1 << 30:
+        _int32("moe_grouped_matmul_mxfp4", E, N, 2 * half)
     if c is None:
         c = a.new_empty((R, N), dtype=out_dtype)
     else:
