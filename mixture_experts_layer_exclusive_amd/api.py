@@ -874,7 +874,8 @@ def quantize_rows_mxfp4(src: torch.Tensor, codes: Optional[torch.Tensor] = None,
 def dequantize_rows_mxfp4(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.bfloat16,
                           out: Optional[torch.Tensor] = None):
     """The numbers that ``quantize_rows_mxfp4``'s codes and scales stand for:
-    [rows, cols] of ``dtype`` (bf16 or fp32; exact in both)."""
+    [rows, cols] of ``dtype`` (bf16 or fp32; exact in both, but for overflow to
+    infinity above 2^128)."""
     if codes.dim() != 2:
         raise ValueError("codes must be [rows, cols / 2]")
     if dtype not in _DTYPES:

@@ -122,7 +122,7 @@ __global__ __launch_bounds__(256) void combine_f32_kernel(const float* __restric
 // Rows of more than 64 lanes are read and written past the caches, short ones (whose ends
 // share cache lines) are read through them, those of 16 lanes also written (30000 tokens,
 // 8 slots of 33 floats: 19 us for 27; 512 floats and more gain nothing).
-// Bound by memory: 32768 tokens, 8 slots of 2048 bf16, 2.28 GB in 394 to 426 us (5.4 to 5.8
+// Bound by memory: 32768 tokens, 8 slots of 2048 bf16, 2.28 GB in 413 to 421 us (5.4 to 5.5
 // TB/s, a copy 6.0), 449 with 4 slots at a time through the caches; 30000 tokens of 128 bf16
 // 23 us, at a copy's rate 22.6; 1023 floats, whose rows begin inside cache lines, 10000
 // tokens 149, at a copy's rate 118.
@@ -278,7 +278,9 @@ hipError_t start_combine_backward(const moe_problem_t& p, const void* dy, const 
     // As many lanes as the row can use.  30000 tokens, 8 slots, with 16, 64 and 256 lanes:
     // 64 bf16 (8 chunks) 16, 27 and 66 us, 128 27, 31 and 66, 192 40, 40 and 66, 256 52, 50
     // and 68, 512 (64 chunks) 101, 96 and 89; 33 floats 27, 40 and 84, 130 120, 74 and 96;
-    // 100 tokens of 512 bf16 7.7, 4.9 and 4.7 (all past the caches).  And a token per
+    // 100 tokens of 512 bf16 7.7, 4.9 and 4.7 (all past the caches).  (With one slot 204
+    // floats, 51 chunks, keep 51 of 256 lanes busy: 21135 tokens 26 us, at a copy's rate
+    // 8.8.)  And a token per
     // compute unit with 256 and 1024 lanes: 38 tokens, 8 slots of 7168 floats 18 and 10 us,
     // 200 of 4096 floats 17 and 12, of 2048 9.6 and 7.9; 500 of 2048 14 and 16.
     const int chunks = (p.d + V - 1) / V;

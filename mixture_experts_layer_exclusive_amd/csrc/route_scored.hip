@@ -11,8 +11,13 @@
 // logits, which then stand for it (unless groups are valued by sums).
 //
 // For k <= 16 the choice is made in 32 bits by G lanes per token, and where it hangs
-// on a difference that 32 bits may have got wrong (about one token in 300), the whole
-// wave makes that token's choice again in 64 bits.
+// on a difference that 32 bits may have got wrong, the whole wave makes that token's choice
+// again in 64 bits.  How often depends on the logits: with a bias about one token in 1000;
+// by groups valued by sums without one, where scores near their end (1, or 0) are alike,
+// most tokens of wide logits.  32768 x 256 in 8 groups of which 4 stay, k = 8, normal logits
+// of standard deviation 2, 4, 6, 8: sigmoid 0.3, 11, 95 and 100 % of the tokens, 27, 48, 100
+// and 98 us; softmax 0.2, 1.3, 10 and 28 %, 26, 32, 49 and 70 us; with a bias 24 to 26 us all.
+// Equal scores that compete always go there.
 #include <float.h>
 #include <math.h>
 
@@ -375,17 +380,20 @@ __global__ __launch_bounds__(256) void route_scored_wave_kernel(moe_gating_t g, 
 // Errors, u = 2^-24.  Sigmoid: exp2 of the rounded product l log2(e) is off by (|l| + 2) u
 // of itself, which counts s (1 - s) times in s, and |l| s (1 - s) < 1 / 4; the sum and the
 // reciprocal add 3 u s: together below 4 u, 8 u for a difference of two.  Softmax: (2 |l - max|
-// + 2) u of s, where |l - max| s < max s, and the quotient 1 u; its sum's error, 24 u, is the
-// same share of all of a token's s, so it counts once in a difference: 24 u + 2 * 5 u of max s,
-// below 2^-18.9.  The sum with the bias adds 2 u |c| to a difference.  A choice is taken for
-// certain if all that it compared differs by more than 2^-20 (softmax: 2^-18 max s) + 2^-22
-// max |c|, twice that for groups (sums of two), else it is made again in 64 bits.
+// + 2) u of s, where |l - max| s < max s, and the quotient 1 u; its sum's error, 20 roundings
+// and its terms' own (2 |l - max| + 2, below 9 in the mean over the scores of 256 experts),
+// 30 u, is the same share of all of a token's s, so it counts once in a difference: 30 u + 2 *
+// 5 u of max s, below 2^-18.6.  The sum with the bias adds 2 u |c| to a difference.  A choice
+// is taken for certain if all that it compared differs by more than 2^-20 (softmax: 2^-18 max
+// s) + 2^-22 max |c|, twice that for groups (sums of two), else it is made again in 64 bits.
 //
 // Bound by instructions (about 1000 for the 4 tokens of a wave, a third of them the lists'),
-// not by the logits' bytes: 32768 tokens, 256 experts, k = 8: 14 us by logits or scores (6 us
-// for the bytes at a copy's rate), 20 with a bias, 24 in 8 groups, of which 4 the certainty's
-// checks and a few tokens' second choice, and 29 with score sums; one token 5.3 us.  A whole
-// wave per token in 64 bits took 161 us.
+// not by the logits' bytes: 32768 tokens, 256 experts, k = 8: 15 us by logits or scores (6 us
+// for the bytes at a copy's rate), 20 with a bias, 26 in 8 groups, of which 4 the certainty's
+// checks and a few tokens' second choice, and 27 with partial score sums, whose adding takes
+// 4; one token 5.3 us.  A whole wave per token in 64 bits took 161 us.  Of 16 experts per lane
+// 2 to 5 values are spilled, and where E is no multiple of 4 the row lies in scratch memory
+// (load_experts).
 constexpr int kMaxRounds = 32;  // of tokens that a workgroup takes one after the other
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -393,7 +401,9 @@ typedef float f32x4_any_t __attribute__((ext_vector_type(4), aligned(4)));
 
 // Values e0 .. e0 + EPL - 1 of a row of E >= 4, in 16-byte loads whatever the row's
 // alignment (4-byte loads: 250 experts 48 us for 36).  The last load of a row ends with it;
-// unless E is a multiple of 4 (VEC), what it holds is moved down.  Values past the row are
+// unless E is a multiple of 4 (VEC), what it holds is moved down, which the compiler makes
+// an indexed read of the array: it lies in scratch memory (48 to 96 bytes per lane), and 250
+// experts take 39 us where 256 take 23 (39008 tokens, a bias, k = 8).  Values past the row are
 // any.
 template <int EPL, bool VEC>
 __device__ __forceinline__ void load_experts(const float* __restrict__ row, int e0, int E, float (&v)[EPL]) {
