@@ -340,7 +340,8 @@ moe_status_t moe_route_scored_workspace_size(const moe_gating_t* g, size_t* byte
  * Whatever the inputs, a token's ids are k different experts.
  * logits_in, x, w_router and logits_out as in moe_route (there bf16 needs d to
  * be a multiple of 64 below 2^25, float32 at most 2^30).  Limits: E and k as
- * everywhere, T <= 2^24 - 1 and T*k <= 2^31 - 1; groups divides E, and k <= groups_kept * (E / groups).
+ * everywhere, T <= 2^24 - 1 and T*k <= 2^31 - 1; groups divides E, and k <=
+ * groups_kept * (E / groups).
  * Workspace: moe_route_scored_workspace_size if score_sums is given, else not
  * looked at.  T = 0 writes zeros to score_sums and nothing else.  No atomics:
  * the same inputs give the same bits.

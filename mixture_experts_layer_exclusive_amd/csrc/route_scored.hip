@@ -396,6 +396,7 @@ __global__ __launch_bounds__(256) void route_scored_wave_kernel(moe_gating_t g, 
 // (load_experts).
 constexpr int kMaxRounds = 32;  // of tokens that a workgroup takes one after the other
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLeastLogit = -709.78f;  // sigmoid scores of lower ones are 0 in 64 bits: exp(-l) overflows
 
 typedef float f32x4_any_t __attribute__((ext_vector_type(4), aligned(4)));
 
@@ -662,9 +663,11 @@ __global__ __launch_bounds__(256, KM == 16 || (EPL == 16 && !VEC) ? 3 : 4) void 
         }
         total = reduce<G>(total, Add());
         // Scores chosen by a bias may be denormals or zeros in 32 bits, their shares are not:
-        // such a token's gates are made in 64 bits, with its choice.  (Not a row of minus
-        // infinities, whose softmax scores are zeros in any number of bits.)
-        sure = sure && !(g.renormalise && total < 0x1p-26f && inv != 0.f);
+        // such a token's gates are made in 64 bits, with its choice.  (Not masked rows,
+        // whose scores are zeros in 64 bits, too: a softmax of minus infinities, and sigmoids
+        // of which the largest logit, the list's first where logits choose, is too low.)
+        sure = sure && !(g.renormalise && total < 0x1p-26f && inv != 0.f &&
+                         !(by_logit && key_value(list[0]) < kLeastLogit));
         if (has && sure) {
 #pragma unroll
             for (int u = 0; u < SLOTS; ++u) {
@@ -766,9 +769,6 @@ __device__ __forceinline__ void sigmoid_parts(float l, float& s, float& rest) {
     rest = l >= 0.f ? x * p : p;
     if (!(l == l)) s = rest = l;
 }
-
-// Sigmoid scores of logits below it are 0 in 64 bits: exp(-l) overflows.
-constexpr float kLeastLogit = -709.78f;
 
 template <int G, bool VEC, typename O>
 __global__ __launch_bounds__(256) void route_scored_backward_kernel(moe_gating_t g, const float* __restrict__ logits,
